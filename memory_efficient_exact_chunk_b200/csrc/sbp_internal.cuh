@@ -329,4 +329,53 @@ cudaError_t embed_bwd(int64_t rows, int64_t cols, int64_t vocab, const int* ids,
                       float* dtable, int* ws, cudaStream_t st);
 size_t embed_bwd_ws_ints(int64_t rows, int64_t vocab);
 
+// scaled embedding and its gradient by sorted tokens (embedding.cu)
+constexpr int64_t kEmbedMaxVocab = (int64_t)1 << 22;
+cudaError_t embed_scaled_fwd(int64_t rows, int64_t cols, int64_t vocab, int dt, float scale,
+                             const int* ids, const void* table, void* y, cudaStream_t st);
+size_t embed_scaled_bwd_ws_bytes(int64_t rows, int64_t cols, int64_t vocab);
+cudaError_t embed_scaled_bwd(int64_t rows, int64_t cols, int64_t vocab, float scale,
+                             const int* ids, const float* dy, float* d_table, int accumulate,
+                             void* ws, cudaStream_t st);
+
+// per-head RMS norm of queries and keys with RoPE (qk_norm.cu)
+struct QkNormHeads {       // the queries or the keys; strides in elements between rows
+  int64_t n = 0;           // heads per row (0: absent)
+  const void* x = nullptr;     // [rows, n, hd], dt
+  int64_t ldx = 0;
+  const void* g = nullptr;     // gain [hd], dt
+  void* y = nullptr;           // forward output, dt
+  int64_t ldy = 0;
+  const float* dy = nullptr;   // backward: upstream gradient and result
+  int64_t lddy = 0;
+  float* dx = nullptr;
+  int64_t lddx = 0;
+};
+struct QkNorm {
+  int64_t rows = 0, hd = 0;
+  int dt = DT_F32;
+  float eps = 0.f;
+  QkNormHeads q, k;
+  // position of row r: positions[r], else pos0 + r % seq_len; rows outside the tables' table_len
+  // positions become zero
+  const int* positions = nullptr;
+  int64_t seq_len = 1, pos0 = 0, table_len = 0;
+  const float *cosb = nullptr, *sinb = nullptr;
+  // > 0: row r of the keys' output is row (r / seq_len) k_T + pos0 + r % seq_len of k.y (the K
+  // prefix of a batch of sequences)
+  int64_t k_T = 0;
+};
+cudaError_t qk_norm_rope_fwd(const QkNorm& a, cudaStream_t st);
+size_t qk_norm_bwd_partial_floats(int64_t rows, int64_t n_heads, int64_t n_kv, int64_t hd);
+cudaError_t qk_norm_rope_bwd(const QkNorm& a, float* dq_g, float* dk_g, float* partial,
+                             cudaStream_t st);
+
+// global gradient norm and clipping (grad_norm.cu); host arrays of device pointers
+size_t grad_norm_ws_bytes(int64_t n);
+cudaError_t grad_sqsum(int64_t n, const float* const* grads, const int64_t* numel, double* sqsum,
+                       void* ws, cudaStream_t st);
+cudaError_t grad_clip(int64_t n, const float* const* grads, float* const* outs,
+                      const int64_t* numel, const double* sqsum, float max_norm, float* norm_out,
+                      cudaStream_t st);
+
 }  // namespace sbp

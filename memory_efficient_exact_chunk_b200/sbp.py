@@ -29,7 +29,11 @@ EXPORTS = [
     "sbp_debug_attn_fwd_bf16", "sbp_debug_attn_bwd_bf16", "sbp_lmhead_ce_forward_stream",
     "sbp_dpo_workspace_size", "sbp_dpo_token_weights", "sbp_lmhead_ce_workspace_size_host",
     "sbp_lmhead_ce_backward_stream_host", "sbp_decoder_layer_backward_stream_reverse",
-    "sbp_debug_gemm_stall_bf16",
+    "sbp_debug_gemm_stall_bf16", "sbp_embedding_scaled_forward",
+    "sbp_embedding_scaled_backward_workspace_size", "sbp_embedding_scaled_backward",
+    "sbp_rope_table", "sbp_qk_norm_rope_forward", "sbp_qk_norm_rope_backward_workspace_size",
+    "sbp_qk_norm_rope_backward", "sbp_grad_norm_workspace_size", "sbp_grad_sqsum",
+    "sbp_grad_clip", "sbp_grad_clip_norm",
 ]
 
 WEIGHT_FIELDS = ("ln1_g", "wq", "wk", "wv", "bq", "bk", "bv", "wo", "ln2_g", "w_gate", "w_up",
@@ -60,6 +64,12 @@ class LayerWeights(C.Structure):
 
 class LayerGrads(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in WEIGHT_FIELDS]
+
+
+class QkCfg(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("n_heads", C.c_int64), ("n_kv_heads", C.c_int64),
+                ("head_dim", C.c_int64), ("seq_len", C.c_int64), ("table_len", C.c_int64),
+                ("eps", C.c_float), ("dtype", C.c_int)]
 
 
 _lib = None
@@ -111,6 +121,23 @@ def load(path: Optional[str] = None):
     lib.sbp_embedding_backward_workspace_size.restype = sz
     lib.sbp_embedding_backward_workspace_size.argtypes = [i64, i64]
     lib.sbp_embedding_backward.argtypes = [i64, i64, i64, vp, vp, vp, vp, sz, vp]
+    lib.sbp_embedding_scaled_forward.argtypes = [i64, i64, i64, C.c_int, C.c_float, vp, vp, vp, vp]
+    lib.sbp_embedding_scaled_backward_workspace_size.restype = sz
+    lib.sbp_embedding_scaled_backward_workspace_size.argtypes = [i64, i64, i64]
+    lib.sbp_embedding_scaled_backward.argtypes = [i64, i64, i64, C.c_float, vp, vp, vp, C.c_int,
+                                                  vp, sz, vp]
+    lib.sbp_rope_table.argtypes = [i64, i64, C.c_double, vp, vp, vp]
+    lib.sbp_qk_norm_rope_forward.argtypes = [C.POINTER(QkCfg), vp, i64, vp, i64] + [vp] * 5 + \
+        [vp, i64, vp, i64, vp]
+    lib.sbp_qk_norm_rope_backward_workspace_size.restype = sz
+    lib.sbp_qk_norm_rope_backward_workspace_size.argtypes = [C.POINTER(QkCfg)]
+    lib.sbp_qk_norm_rope_backward.argtypes = [C.POINTER(QkCfg), vp, i64, vp, i64] + [vp] * 5 + \
+        [vp, i64] * 4 + [vp, vp, vp, sz, vp]
+    lib.sbp_grad_norm_workspace_size.restype = sz
+    lib.sbp_grad_norm_workspace_size.argtypes = [i64]
+    lib.sbp_grad_sqsum.argtypes = [i64, vp, vp, vp, vp, sz, vp]
+    lib.sbp_grad_clip.argtypes = [i64, vp, vp, vp, vp, C.c_float, vp, vp]
+    lib.sbp_grad_clip_norm.argtypes = [i64, vp, vp, vp, C.c_float, vp, vp, sz, vp]
     lib.sbp_debug_gemm_bf16.argtypes = [i64, i64, i64, vp, C.c_int, i64, vp, C.c_int, i64, vp, i64,
                                          C.c_int, C.c_int, i64, vp, vp]
     lib.sbp_lmhead_ce_backward_noalloc.argtypes = [i64, i64, i64, C.c_int, C.c_int] + [vp] * 7 + \
@@ -343,6 +370,246 @@ def embedding_backward(ids, dy2d, d_table, ws=None, stream=None):
         ws = workspace(need, dy2d.device)
     _check(load().sbp_embedding_backward(rows, cols, V, _ptr(ids), _ptr(dy2d), _ptr(d_table),
                                          _ptr(ws), ws.numel(), _stream(stream)))
+    return ws
+
+
+# ----------------------------------------------------------------------------- step operators
+def _device_of(stream, tensors):
+    """The one CUDA device of `tensors` (None entries are left out).  The library launches on
+    the current device, so the tensors and the stream have to be on it."""
+    torch = _torch()
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on two devices, {dev} and {t.device}")
+    cur = torch.cuda.current_device()
+    if dev.index != cur or (stream is not None and stream.device != dev):
+        raise ValueError(f"tensors on {dev}: the current device and the stream must be its")
+    return dev
+
+
+def _is(t, name, dtype, shape):
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+
+
+def _step_ws(ws, need, dev):
+    if need == 0:
+        raise SbpError(1, "invalid sizes")
+    if ws is None or ws.numel() * ws.element_size() < need:
+        return workspace(need, dev)
+    if not ws.is_contiguous() or ws.device != dev:
+        raise ValueError(f"the workspace must be a contiguous buffer on {dev}")
+    return ws
+
+
+def _nbytes(t):
+    return t.numel() * t.element_size()
+
+
+def embedding_scaled_forward(ids, table, scale, y, stream=None):
+    """y[r] = scale * table[ids[r]]; ids int32, any shape; ids outside [0, vocab) give zero rows
+    (include/sbp_step.h)."""
+    torch = _torch()
+    V, cols = table.shape
+    rows = ids.numel()
+    dt = _dtype_code(table)
+    _is(ids, "ids", torch.int32, ids.shape)
+    _is(table, "table", table.dtype, (V, cols))
+    _is(y, "y", table.dtype, (rows, cols) if y.dim() == 2 else (*ids.shape, cols))
+    _device_of(stream, (ids, table, y))
+    _check(load().sbp_embedding_scaled_forward(rows, cols, V, dt, scale, _ptr(ids), _ptr(table),
+                                               _ptr(y), _stream(stream)))
+
+
+def embedding_scaled_backward(ids, dy, scale, d_table, accumulate=True, ws=None, stream=None):
+    """d_table (+)= scale * the sum of dy's rows of each id, by sorted tokens; without
+    `accumulate` the whole table is written.  Returns the workspace, to be passed again."""
+    torch = _torch()
+    V, cols = d_table.shape
+    rows = ids.numel()
+    _is(ids, "ids", torch.int32, ids.shape)
+    _is(d_table, "d_table", torch.float32, (V, cols))
+    _is(dy, "dy", torch.float32, (rows, cols) if dy.dim() == 2 else (*ids.shape, cols))
+    dev = _device_of(stream, (ids, dy, d_table))
+    lib = load()
+    ws = _step_ws(ws, lib.sbp_embedding_scaled_backward_workspace_size(rows, cols, V), dev)
+    _check(lib.sbp_embedding_scaled_backward(rows, cols, V, scale, _ptr(ids), _ptr(dy),
+                                             _ptr(d_table), int(accumulate), _ptr(ws),
+                                             _nbytes(ws), _stream(stream)))
+    return ws
+
+
+def rope_table(n_positions, head_dim, theta, device="cuda", stream=None):
+    """(cos, sin) tables [n_positions, head_dim // 2] fp32 of the decoder layer's RoPE."""
+    torch = _torch()
+    if n_positions < 1 or head_dim < 2:
+        raise ValueError("rope_table: need positive sizes")
+    cos = torch.empty(n_positions, head_dim // 2, dtype=torch.float32, device=device)
+    sin = torch.empty_like(cos)
+    _device_of(stream, (cos,))
+    _check(load().sbp_rope_table(n_positions, head_dim, theta, _ptr(cos), _ptr(sin),
+                                 _stream(stream)))
+    return cos, sin
+
+
+def _heads(t, name, dtype, shape):
+    """Row stride of a [rows, heads, head_dim] tensor whose rows may lie apart."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    rows, n, hd = shape
+    sr, sh, s1 = t.stride()
+    if s1 != 1 or (n > 1 and sh != hd):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    if rows == 1:
+        return n * hd
+    if sr < n * hd:
+        raise ValueError(f"{name}: the rows overlap")
+    return sr
+
+
+def _qk_call(q, k, q_g, k_g, cos, sin, eps, positions, seq_len, stream):
+    """Checks of what both directions share; the configuration and the leading arguments."""
+    torch = _torch()
+    rows, H, hd = q.shape
+    Hkv = 0 if k is None else k.shape[1]
+    dt = _dtype_code(q)
+    ldq = _heads(q, "q", q.dtype, (rows, H, hd))
+    _is(q_g, "q_g", q.dtype, (hd,))
+    ldk = 0
+    if k is not None:
+        ldk = _heads(k, "k", q.dtype, (rows, Hkv, hd))
+        _is(k_g, "k_g", q.dtype, (hd,))
+    table_len = cos.shape[0]
+    _is(cos, "cos", torch.float32, (table_len, hd // 2))
+    _is(sin, "sin", torch.float32, (table_len, hd // 2))
+    if positions is not None:
+        _is(positions, "positions", torch.int32, (rows,))
+    cfg = QkCfg(rows, H, Hkv, hd, seq_len if seq_len is not None else rows, table_len, eps, dt)
+    return cfg, (C.byref(cfg), _ptr(q), ldq, _ptr(k), ldk, _ptr(q_g),
+                 _ptr(k_g) if k is not None else None, _ptr(positions), _ptr(cos), _ptr(sin))
+
+
+def qk_norm_rope_forward(q, k, q_g, k_g, cos, sin, eps, q_out, k_out, positions=None,
+                         seq_len=None, stream=None):
+    """Per-head RMS norm with RoPE of q [rows, heads, head_dim] and k [rows, kv_heads, head_dim]
+    (rows may be strided, k may be None) into q_out and k_out, which may be q and k
+    (include/sbp_step.h).  The position of row r is positions[r], or r % seq_len (default: r)."""
+    cfg, args = _qk_call(q, k, q_g, k_g, cos, sin, eps, positions, seq_len, stream)
+    ldqo = _heads(q_out, "q_out", q.dtype, q.shape)
+    ldko = 0 if k is None else _heads(k_out, "k_out", q.dtype, k.shape)
+    _device_of(stream, (q, k, q_g, k_g, cos, sin, positions, q_out, k_out))
+    _check(load().sbp_qk_norm_rope_forward(*args, _ptr(q_out), ldqo,
+                                           _ptr(k_out) if k is not None else None, ldko,
+                                           _stream(stream)))
+
+
+def qk_norm_rope_backward(q, k, q_g, k_g, cos, sin, eps, dq_out, dk_out, dq, dk, dq_g, dk_g,
+                          positions=None, seq_len=None, ws=None, stream=None):
+    """Backward of qk_norm_rope_forward from its inputs: dq, dk overwritten (they may be dq_out,
+    dk_out), dq_g, dk_g accumulated; all gradients fp32.  Returns the workspace."""
+    torch = _torch()
+    f32 = torch.float32
+    cfg, args = _qk_call(q, k, q_g, k_g, cos, sin, eps, positions, seq_len, stream)
+    hd = q.shape[2]
+    ld = [_heads(dq_out, "dq_out", f32, q.shape), _heads(dq, "dq", f32, q.shape), 0, 0]
+    _is(dq_g, "dq_g", f32, (hd,))
+    if k is None:
+        dk_out = dk = dk_g = None
+    else:
+        ld[2:] = [_heads(dk_out, "dk_out", f32, k.shape), _heads(dk, "dk", f32, k.shape)]
+        _is(dk_g, "dk_g", f32, (hd,))
+    dev = _device_of(stream, (q, k, q_g, k_g, cos, sin, positions, dq_out, dk_out, dq, dk, dq_g,
+                              dk_g))
+    lib = load()
+    ws = _step_ws(ws, lib.sbp_qk_norm_rope_backward_workspace_size(C.byref(cfg)), dev)
+    _check(lib.sbp_qk_norm_rope_backward(*args, _ptr(dq_out), ld[0], _ptr(dk_out), ld[2],
+                                         _ptr(dq), ld[1], _ptr(dk), ld[3], _ptr(dq_g),
+                                         _ptr(dk_g), _ptr(ws), _nbytes(ws), _stream(stream)))
+    return ws
+
+
+class GradList:
+    """The gradients of a model in the form the norm and the clipping take: checked once, their
+    pointers and sizes in host arrays.  It holds the tensors."""
+
+    def __init__(self, tensors):
+        torch = _torch()
+        self.tensors = list(tensors)
+        n = len(self.tensors)
+        for i, t in enumerate(self.tensors):
+            _is(t, f"gradient {i}", torch.float32, t.shape)
+            if not t.is_cuda or t.device != self.tensors[0].device:
+                raise ValueError(f"gradient {i}: all gradients must be on one CUDA device")
+        self.ptrs = (C.c_void_p * n)(*[t.data_ptr() for t in self.tensors])
+        self.numel = (C.c_int64 * n)(*[t.numel() for t in self.tensors])
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def _grad_args(grads, out, scalars, stream):
+    grads = grads if isinstance(grads, GradList) else GradList(grads)
+    if len(grads) == 0:
+        raise ValueError("no gradients")
+    if out is not None:
+        out = out if isinstance(out, GradList) else GradList(out)
+        if len(out) != len(grads) or list(out.numel) != list(grads.numel):
+            raise ValueError("out must have the gradients' element counts")
+    dev = _device_of(stream, (grads.tensors[0], out.tensors[0] if out is not None else None,
+                              *scalars))
+    return grads, out, dev
+
+
+def grad_norm_workspace_size(n_tensors) -> int:
+    return int(load().sbp_grad_norm_workspace_size(n_tensors))
+
+
+def grad_sqsum(grads, sqsum, ws=None, stream=None):
+    """sqsum[0] (float64) = the sum of the squares of all gradients (a GradList, or a list of
+    fp32 tensors).  Returns the workspace."""
+    grads, _, dev = _grad_args(grads, None, (sqsum,), stream)
+    _is(sqsum, "sqsum", _torch().float64, (1,))
+    ws = _step_ws(ws, grad_norm_workspace_size(len(grads)), dev)
+    _check(load().sbp_grad_sqsum(len(grads), grads.ptrs, grads.numel, _ptr(sqsum), _ptr(ws),
+                                 _nbytes(ws), _stream(stream)))
+    return ws
+
+
+def grad_clip(grads, sqsum, max_norm, norm_out=None, out=None, stream=None):
+    """out (default: in place) = grads * min(1, max_norm / (sqrt(sqsum) + 1e-6))."""
+    torch = _torch()
+    grads, out, _ = _grad_args(grads, out, (sqsum, norm_out), stream)
+    _is(sqsum, "sqsum", torch.float64, (1,))
+    if norm_out is not None:
+        _is(norm_out, "norm_out", torch.float32, (1,))
+    _check(load().sbp_grad_clip(len(grads), grads.ptrs, out.ptrs if out is not None else None,
+                                grads.numel, _ptr(sqsum), max_norm, _ptr(norm_out),
+                                _stream(stream)))
+
+
+def grad_clip_norm(grads, max_norm, norm_out, out=None, ws=None, stream=None):
+    """norm_out[0] = the global norm of all gradients, which are clipped to max_norm (in place,
+    or into `out`).  Returns the workspace."""
+    grads, out, dev = _grad_args(grads, out, (norm_out,), stream)
+    _is(norm_out, "norm_out", _torch().float32, (1,))
+    ws = _step_ws(ws, grad_norm_workspace_size(len(grads)), dev)
+    _check(load().sbp_grad_clip_norm(len(grads), grads.ptrs,
+                                     out.ptrs if out is not None else None, grads.numel,
+                                     max_norm, _ptr(norm_out), _ptr(ws), _nbytes(ws),
+                                     _stream(stream)))
     return ws
 
 
