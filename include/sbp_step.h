@@ -22,6 +22,7 @@ extern "C" {
  * Scaled token embedding:  y[r] = scale * table[ids[r]]   (fp32 product, rounded once to dt)
  *   ids    device int32 [rows]; a row whose id is outside [0, vocab) (padding) becomes zero
  *   table  device [vocab, cols], dt;   y  device [rows, cols], dt
+ * Here and below rows < 2^30, cols <= 2^20 and vocab <= 2^22 (else SBP_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------------------------ */
 sbp_status sbp_embedding_scaled_forward(int64_t rows, int64_t cols, int64_t vocab, sbp_dtype dt,
                                         float scale, const int32_t* ids, const void* table,
@@ -34,7 +35,7 @@ sbp_status sbp_embedding_scaled_forward(int64_t rows, int64_t cols, int64_t voca
  * fixed blocks of the sorted list, the block sums in order.  Without `accumulate` the whole
  * table is written (ids that do not occur get zeros): no clearing pass is needed.  Rows whose id
  * is outside [0, vocab) are skipped; their dy is not read.  dy fp32 [rows, cols], d_table fp32
- * [vocab, cols].  rows < 2^30; vocab <= 2^22 (else SBP_ERR_UNSUPPORTED).
+ * [vocab, cols].
  */
 size_t sbp_embedding_scaled_backward_workspace_size(int64_t rows, int64_t cols, int64_t vocab);
 sbp_status sbp_embedding_scaled_backward(int64_t rows, int64_t cols, int64_t vocab, float scale,

@@ -11,109 +11,576 @@ namespace sbp {
 
 namespace {
 
-inline unsigned nblk(int64_t n, int64_t t) { return (unsigned)((n + t - 1) / t); }
+inline int64_t nblk(int64_t n, int64_t t) { return (n + t - 1) / t; }
+
+constexpr int kThreads = 256;
+
+// ---------------------------------------------------------------- vectors of V elements
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+  T v[V];
+};
+
+// widest vector (elements) with which a row of cols elements of es bytes stays aligned
+int vec_width(int64_t cols, int es) {
+  int v = 16 / es;
+  while (cols % v) v /= 2;
+  return v;
+}
 
 // ---------------------------------------------------------------- forward
-// One CTA per row; a row whose id is outside [0, vocab) becomes zero.
-template <typename T>
-__global__ void embed_scaled_fwd_kernel(int64_t cols, int64_t vocab, float scale,
-                                        const int* __restrict__ ids, const T* __restrict__ table,
-                                        T* __restrict__ y) {
-  const int64_t r = blockIdx.x;
-  const int64_t v = ids[r];
-  const bool ok = v >= 0 && v < vocab;
-  for (int64_t c = threadIdx.x; c < cols; c += blockDim.x)
-    st_f(y, r * cols + c, ok ? scale * ld_f(table, v * cols + c) : 0.f);
+// The rows are one list of cols / V vectors each; a CTA takes kFwdUnroll * 256 consecutive
+// vectors, so that a thread has kFwdUnroll independent loads in flight whatever the row length.
+constexpr int kFwdUnroll = 4;
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads)
+embed_scaled_fwd_kernel(int64_t rows, unsigned nv, int64_t vocab, float scale,
+                        const int* __restrict__ ids, const T* __restrict__ table,
+                        T* __restrict__ y) {
+  const int64_t first = (int64_t)blockIdx.x * (kFwdUnroll * kThreads);
+  const int64_t r0 = first / nv;
+  const unsigned o0 = (unsigned)(first - r0 * nv) + threadIdx.x;
+  const Vec<T, V>* tv = reinterpret_cast<const Vec<T, V>*>(table);
+  Vec<T, V>* yv = reinterpret_cast<Vec<T, V>*>(y);
+  Vec<T, V> x[kFwdUnroll];
+  bool ok[kFwdUnroll];
+#pragma unroll
+  for (int k = 0; k < kFwdUnroll; ++k) {
+    const unsigned o = o0 + k * kThreads, dr = o / nv;
+    const int64_t r = r0 + dr;
+    const int64_t v = r < rows ? ids[r] : -1;
+    ok[k] = v >= 0 && v < vocab;
+    if (ok[k]) x[k] = tv[v * nv + (o - dr * nv)];
+  }
+#pragma unroll
+  for (int k = 0; k < kFwdUnroll; ++k) {
+    const int64_t i = first + threadIdx.x + k * kThreads;
+    if (i >= rows * nv) break;
+#pragma unroll
+    for (int j = 0; j < V; ++j) st_f(x[k].v, j, ok[k] ? scale * ld_f(x[k].v, j) : 0.f);
+    yv[i] = x[k];
+  }
 }
 
 // ---------------------------------------------------------------- sort by id
-// Sorted position of every row by counting: a row's run starts at the number of rows with a
-// smaller id and the row stands behind the earlier rows of its own id (a stable sort).  Ids
-// outside [0, vocab) take the key vocab and end up last.  Four threads share a row; the ids
-// pass through shared memory.
-constexpr int kRankThreads = 256, kRankRows = kRankThreads / 4, kRankTile = 4096;
-__global__ void __launch_bounds__(kRankThreads)
-embed_rank_kernel(int rows, int vocab, const int* __restrict__ ids, int4* __restrict__ sorted) {
-  __shared__ __align__(16) int key[kRankTile];
-  const int r = blockIdx.x * kRankRows + threadIdx.x / 4, part = threadIdx.x % 4;
-  int mine = -1;
-  if (r < rows) {
-    mine = ids[r];
-    if (mine < 0 || mine >= vocab) mine = vocab;
+// What the accumulation reads of a sorted position: its row, and its run (the positions with the
+// same id): where it starts and how long it is, and the id.
+//   sorted[p] = {row, start, length, id},  p in [0, *n_valid); rows of ids outside [0, vocab)
+// are left out.  present[v] (where it is wanted) tells whether id v occurs.
+
+// Few rows: the sorted position of every row by counting.  A run starts at the number of rows
+// with a smaller id, and a row stands behind the earlier rows of its own id.  Sixteen threads
+// share a row; the ids pass through shared memory.  rows^2 comparisons: 2 us at 4096 rows, where
+// the three launches of the digit sort below take longer.
+constexpr int64_t kRankRows = 4096;
+constexpr int kRankShare = 16, kRankPerCta = kThreads / kRankShare;
+__global__ void __launch_bounds__(kThreads)
+embed_rank_kernel(int rows, int vocab, const int* __restrict__ ids, int4* __restrict__ sorted,
+                  int* __restrict__ n_valid, unsigned char* __restrict__ present) {
+  __shared__ __align__(16) int key[kRankRows];
+  for (int i = threadIdx.x; i < rows; i += kThreads) {
+    const int v = ids[i];
+    key[i] = v < 0 || v >= vocab ? vocab : v;
   }
+  __syncthreads();
+  const int r = blockIdx.x * kRankPerCta + threadIdx.x / kRankShare;
+  const int part = threadIdx.x % kRankShare;
+  const int mine = r < rows ? key[r] : vocab;
   int less = 0, equal = 0, before = 0;
-  for (int t0 = 0; t0 < rows; t0 += kRankTile) {
-    const int n = min(kRankTile, rows - t0);
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kRankThreads) {
-      const int v = ids[t0 + i];
-      key[i] = v < 0 || v >= vocab ? vocab : v;
-    }
-    __syncthreads();
-    for (int i = part; i < n; i += 4) {
-      const int k = key[i];
-      less += k < mine;
-      equal += k == mine;
-      before += k == mine && t0 + i < r;
-    }
+#pragma unroll 4
+  for (int i = part; i < rows; i += kRankShare) {
+    const int k = key[i];
+    less += k < mine;
+    equal += k == mine;
+    before += k == mine && i < r;
   }
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
+  for (int o = 1; o < kRankShare; o <<= 1) {
     less += __shfl_xor_sync(0xffffffffu, less, o);
     equal += __shfl_xor_sync(0xffffffffu, equal, o);
     before += __shfl_xor_sync(0xffffffffu, before, o);
   }
-  if (r < rows && part == 0) sorted[less + before] = make_int4(r, less, equal, mine);
+  if (part == 0 && r < rows && mine < vocab) {
+    sorted[less + before] = make_int4(r, less, equal, mine);
+    if (present && before == 0) present[mine] = 1;
+  }
+  if (blockIdx.x == 0) {
+    __shared__ int red[kThreads / 32];
+    int n = 0;
+    for (int i = threadIdx.x; i < rows; i += kThreads) n += key[i] < vocab;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = n;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < kThreads / 32; ++w) n += red[w];
+      *n_valid = n;
+    }
+  }
+}
+
+// Many rows: the rows are dealt to kBuckets buckets by the low digit of their id, then each
+// bucket is sorted by the rest of the id by one CTA (neighbouring ids, of which a vocabulary
+// numbered by frequency has its most frequent at the low end, fall into different buckets).
+// Both steps are counting sorts that keep the rows' order without atomics: every warp takes a
+// contiguous piece, counts its keys in a histogram of its own, and after a scan over (key, warp)
+// places them; inside a warp equal keys are ranked by lane.
+constexpr int kBuckets = 512, kDealThreads = 512, kDealWarps = kDealThreads / 32;
+constexpr int64_t kDealMinRows = 2048, kDealMaxBlocks = 128;   // rows of a block at least; blocks
+
+__device__ __forceinline__ bool valid_id(int v, int vocab) { return v >= 0 && v < vocab; }
+
+// counts[block][bucket]
+__global__ void __launch_bounds__(kDealThreads)
+embed_count_kernel(int rows, int per_block, int vocab, const int* __restrict__ ids,
+                   int* __restrict__ counts) {
+  __shared__ int hist[kBuckets];
+  hist[threadIdx.x] = 0;
+  __syncthreads();
+  const int r0 = blockIdx.x * per_block, r1 = min(rows, r0 + per_block);
+  for (int r = r0 + threadIdx.x; r < r1; r += kDealThreads) {
+    const int v = ids[r];
+    if (valid_id(v, vocab)) atomicAdd(&hist[v % kBuckets], 1);
+  }
+  __syncthreads();
+  counts[blockIdx.x * kBuckets + threadIdx.x] = hist[threadIdx.x];
+}
+
+// exclusive scan of one value per thread over the block (any multiple of 32 threads)
+__device__ __forceinline__ int block_exclusive_scan(int v, int* red) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += t;
+  }
+  __syncthreads();
+  if (lane == 31) red[wid] = s;
+  __syncthreads();
+  int base = 0;
+  for (int w = 0; w < wid; ++w) base += red[w];
+  return base + s - v;
+}
+
+// dealt[...] = {id, row} by bucket, rows in order; base[b] = start of bucket b, base[kBuckets] =
+// number of valid rows
+__global__ void __launch_bounds__(kDealThreads)
+embed_deal_kernel(int rows, int per_block, int vocab, const int* __restrict__ ids,
+                  const int* __restrict__ counts, int2* __restrict__ dealt,
+                  int* __restrict__ base) {
+  __shared__ int hist[kDealWarps][kBuckets];
+  __shared__ int red[kDealWarps];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int b = threadIdx.x;                      // one bucket per thread in the scans
+  int total = 0, before = 0;
+#pragma unroll 8
+  for (int k = 0; k < (int)gridDim.x; ++k) {
+    const int c = counts[k * kBuckets + b];
+    total += c;
+    if (k < (int)blockIdx.x) before += c;
+  }
+#pragma unroll
+  for (int w = 0; w < kDealWarps; ++w) hist[w][b] = 0;
+  const int start = block_exclusive_scan(total, red);
+  if (blockIdx.x == 0) {
+    base[b] = start;
+    if (b == kBuckets - 1) base[kBuckets] = start + total;
+  }
+  __syncthreads();
+  const int per_warp = per_block / kDealWarps;    // per_block is a multiple of 512
+  const int r0 = blockIdx.x * per_block + wid * per_warp;
+  for (int i = 0; i < per_warp; i += 32) {
+    const int r = r0 + i + lane;
+    const int v = r < rows ? ids[r] : -1;
+    const int key = valid_id(v, vocab) ? v % kBuckets : kBuckets;
+    const unsigned same = __match_any_sync(0xffffffffu, key);
+    if (key < kBuckets && (same & ((1u << lane) - 1)) == 0) hist[wid][key] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  int at = start + before;
+#pragma unroll
+  for (int w = 0; w < kDealWarps; ++w) {
+    const int c = hist[w][b];
+    hist[w][b] = at;
+    at += c;
+  }
+  __syncthreads();
+  for (int i = 0; i < per_warp; i += 32) {
+    const int r = r0 + i + lane;
+    const int v = r < rows ? ids[r] : -1;
+    const int key = valid_id(v, vocab) ? v % kBuckets : kBuckets;
+    const unsigned same = __match_any_sync(0xffffffffu, key);
+    const int rank = __popc(same & ((1u << lane) - 1));
+    int pos = 0;
+    if (key < kBuckets) pos = hist[wid][key] + rank;
+    __syncwarp();
+    if (key < kBuckets) {
+      if (rank == 0) hist[wid][key] = pos + __popc(same);
+      dealt[pos] = make_int2(v, r);
+    }
+    __syncwarp();
+  }
+}
+
+// One CTA per bucket: a counting sort by bin = id / kBuckets with `warps` histograms.  Shared
+// memory: hist[warps][bins], start[bins], len[bins].
+__global__ void __launch_bounds__(kThreads)
+embed_bucket_kernel(int vocab, int bins, int warps, const int* __restrict__ base,
+                    const int2* __restrict__ dealt, int4* __restrict__ sorted,
+                    unsigned char* __restrict__ present) {
+  extern __shared__ int sm[];
+  __shared__ int red[kThreads / 32];
+  int* start = sm + warps * bins;
+  int* len = start + bins;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int b0 = base[blockIdx.x], n = base[blockIdx.x + 1] - b0;
+  for (int i = threadIdx.x; i < warps * bins; i += kThreads) sm[i] = 0;
+  __syncthreads();
+  const int per_warp = (n + warps * 32 - 1) / (warps * 32) * 32;
+  const int i0 = b0 + wid * per_warp, i1 = min(b0 + n, i0 + per_warp);
+  int* hist = sm + wid * bins;
+  if (wid < warps) {
+    for (int i = i0; i < i1; i += 32) {
+      const int key = i + lane < i1 ? dealt[i + lane].x / kBuckets : bins;
+      const unsigned same = __match_any_sync(0xffffffffu, key);
+      if (key < bins && (same & ((1u << lane) - 1)) == 0) hist[key] += __popc(same);
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  const int per = (bins + kThreads - 1) / kThreads;
+  const int k0 = min(bins, (int)threadIdx.x * per), k1 = min(bins, k0 + per);
+  int mine = 0;
+  for (int k = k0; k < k1; ++k) {
+    int c = 0;
+    for (int w = 0; w < warps; ++w) c += sm[w * bins + k];
+    len[k] = c;
+    mine += c;
+  }
+  int at = b0 + block_exclusive_scan(mine, red);
+  for (int k = k0; k < k1; ++k) {
+    start[k] = at;
+    for (int w = 0; w < warps; ++w) {
+      const int c = sm[w * bins + k];
+      sm[w * bins + k] = at;
+      at += c;
+    }
+    const int v = k * kBuckets + blockIdx.x;
+    if (present && v < vocab) present[v] = len[k] > 0;
+  }
+  __syncthreads();
+  if (wid < warps) {
+    for (int i = i0; i < i1; i += 32) {
+      const int2 d = i + lane < i1 ? dealt[i + lane] : make_int2(0, 0);
+      const int key = i + lane < i1 ? d.x / kBuckets : bins;
+      const unsigned same = __match_any_sync(0xffffffffu, key);
+      const int rank = __popc(same & ((1u << lane) - 1));
+      int pos = 0;
+      if (key < bins) pos = hist[key] + rank;
+      __syncwarp();
+      if (key < bins) {
+        if (rank == 0) hist[key] = pos + __popc(same);
+        sorted[pos] = make_int4(d.y, start[key], len[key], d.x);
+      }
+      __syncwarp();
+    }
+  }
 }
 
 // ---------------------------------------------------------------- accumulate
-// One CTA per sorted position; the first of each run adds the run's rows in order.
-__global__ void embed_run_kernel(int64_t cols, int vocab, float scale,
-                                 const int4* __restrict__ sorted, const float* __restrict__ dy,
-                                 float* __restrict__ d_table) {
-  const int p = blockIdx.x;
-  const int4 s = sorted[p];
-  if (s.y != p || s.w == vocab) return;
-  for (int64_t c = threadIdx.x; c < cols; c += blockDim.x) {
-    float a = 0.f;
-    for (int i = 0; i < s.z; ++i) a += dy[(int64_t)sorted[p + i].x * cols + c];
-    d_table[(int64_t)s.w * cols + c] += scale * a;
+// A run is cut into units of kUnit rows counted from its start.  A group of `group` threads
+// takes `window` consecutive sorted positions and adds every unit that begins there, all of its
+// rows in order, V columns per thread.  The unit of a run of one unit goes into the table; those
+// of longer runs go to partial rows, which embed_join_kernel adds in order.  In the list of
+// partial rows at most two units begin within kUnit positions: one that continues a run and one
+// that begins the next (a run longer than kUnit leaves room for no third), which gives the slot
+// 2 (p / kUnit) + (p is its run's start).
+constexpr int kUnit = 64;
+
+template <int V>
+__device__ __forceinline__ void vload(const float* p, float (&x)[V]) {
+  const Vec<float, V> t = *reinterpret_cast<const Vec<float, V>*>(p);
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = t.v[i];
+}
+template <int V>
+__device__ __forceinline__ void vstore(float* p, const float (&x)[V]) {
+  Vec<float, V> t;
+#pragma unroll
+  for (int i = 0; i < V; ++i) t.v[i] = x[i];
+  *reinterpret_cast<Vec<float, V>*>(p) = t;
+}
+
+struct AccumArgs {
+  int64_t cols;
+  int rows, vocab;
+  float scale;
+  int accumulate, group, window;
+  int64_t acc_blocks;      // CTAs that accumulate; the ones behind them clear absent rows
+  const int4* sorted;
+  const int* n_valid;
+  const unsigned char* present;
+  const float* dy;
+  float *d_table, *partial;
+};
+
+template <int V>
+__global__ void __launch_bounds__(kThreads)
+embed_accum_kernel(AccumArgs a) {
+  const int64_t c = ((int64_t)blockIdx.y * a.group + threadIdx.x % a.group) * V;
+  const int g = threadIdx.x / a.group, groups = kThreads / a.group;
+  if ((int64_t)blockIdx.x >= a.acc_blocks) {
+    // table rows whose id does not occur
+    const int64_t stride = (int64_t)(gridDim.x - a.acc_blocks) * groups;
+    if (c >= a.cols) return;
+    const float zero[V] = {};
+    for (int64_t v = (blockIdx.x - a.acc_blocks) * groups + g; v < a.vocab; v += stride)
+      if (!a.present[v]) vstore<V>(a.d_table + v * a.cols + c, zero);
+    return;
   }
+  const int n = *a.n_valid;
+  const int64_t p0 = ((int64_t)blockIdx.x * groups + g) * a.window;
+  const int p1 = (int)imin(n, p0 + a.window);
+  if (c >= a.cols) return;
+  for (int p = (int)imin(n, p0); p < p1; ++p) {
+    const int4 s = a.sorted[p];
+    if ((p - s.y) % kUnit != 0) continue;
+    const int e = min(p + kUnit, s.y + s.z);
+    float sum[V];
+    vload<V>(a.dy + (int64_t)s.x * a.cols + c, sum);
+    int i = p + 1;
+    for (; i + 4 <= e; i += 4) {
+      float x[4][V];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) vload<V>(a.dy + (int64_t)a.sorted[i + k].x * a.cols + c, x[k]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum[j] += x[k][j];
+    }
+    for (; i < e; ++i) {
+      float x[V];
+      vload<V>(a.dy + (int64_t)a.sorted[i].x * a.cols + c, x);
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum[j] += x[j];
+    }
+    if (s.z > kUnit) {
+      const int64_t slot = 2 * (int64_t)(p / kUnit) + (p == s.y);
+      vstore<V>(a.partial + slot * a.cols + c, sum);
+      continue;
+    }
+    float* d = a.d_table + (int64_t)s.w * a.cols + c;
+    if (a.accumulate) {
+      float old[V];
+      vload<V>(d, old);
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum[j] = fmaf(a.scale, sum[j], old[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum[j] *= a.scale;
+    }
+    vstore<V>(d, sum);
+  }
+}
+
+// Runs longer than kUnit.  CTA x looks for the run that starts in positions [x kUnit, (x + 1)
+// kUnit) (at most one such run does); each of its warps adds an eighth of the run's partial
+// rows, V columns per lane, and warp 0 joins the eight sums in order.
+template <int V>
+__global__ void __launch_bounds__(kThreads)
+embed_join_kernel(AccumArgs a) {
+  __shared__ float sums[kThreads / 32][32 * V];
+  __shared__ int found;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int n = *a.n_valid;
+  const int p0 = blockIdx.x * kUnit;
+  if (threadIdx.x == 0) found = -1;
+  __syncthreads();
+  if (threadIdx.x < kUnit && p0 + (int)threadIdx.x < n) {
+    const int p = p0 + threadIdx.x;
+    const int4 s = a.sorted[p];
+    if (s.y == p && s.z > kUnit) found = p;
+  }
+  __syncthreads();
+  if (found < 0) return;
+  const int4 s = a.sorted[found];
+  const int units = (s.z + kUnit - 1) / kUnit;
+  const int per = (units + kThreads / 32 - 1) / (kThreads / 32);
+  const int u0 = min(units, wid * per), u1 = min(units, u0 + per);
+  const int64_t c = ((int64_t)blockIdx.y * 32 + lane) * V;
+  float sum[V] = {};
+  if (c < a.cols) {
+#pragma unroll 8
+    for (int u = u0; u < u1; ++u) {
+      const int p = s.y + u * kUnit;
+      float x[V];
+      vload<V>(a.partial + (2 * (int64_t)(p / kUnit) + (u == 0)) * a.cols + c, x);
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum[j] += x[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) sums[wid][lane * V + j] = sum[j];
+  __syncthreads();
+  if (wid != 0 || c >= a.cols) return;
+  for (int w = 1; w < kThreads / 32; ++w)
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum[j] += sums[w][lane * V + j];
+  float* d = a.d_table + (int64_t)s.w * a.cols + c;
+  if (a.accumulate) {
+    float old[V];
+    vload<V>(d, old);
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum[j] = fmaf(a.scale, sum[j], old[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum[j] *= a.scale;
+  }
+  vstore<V>(d, sum);
+}
+
+// ---------------------------------------------------------------- workspace
+struct Plan {
+  int* head;                // number of valid rows, then the buckets' starts
+  int4* sorted;
+  unsigned char* present;
+  int2* dealt;
+  int* counts;
+  float* partial;
+  size_t bytes;
+};
+
+int64_t deal_rows(int64_t rows) {     // rows of a block of the deal, a multiple of 512
+  const int64_t r = nblk(rows, kDealMaxBlocks);
+  return imax(kDealMinRows, nblk(r, kDealThreads) * kDealThreads);
+}
+
+Plan plan(void* ws, int64_t rows, int64_t cols, int64_t vocab) {
+  Plan p;
+  size_t off = 0;
+  auto take = [&](size_t n) {
+    void* q = ws ? static_cast<char*>(ws) + off : nullptr;
+    off += (n + 255) & ~size_t(255);
+    return q;
+  };
+  p.head = static_cast<int*>(take(sizeof(int) * (1 + kBuckets + 1)));
+  p.sorted = static_cast<int4*>(take(sizeof(int4) * rows));
+  p.present = static_cast<unsigned char*>(take(vocab));
+  const bool deal = rows > kRankRows;
+  p.dealt = static_cast<int2*>(take(deal ? sizeof(int2) * rows : 0));
+  p.counts =
+      static_cast<int*>(take(deal ? sizeof(int) * kBuckets * nblk(rows, deal_rows(rows)) : 0));
+  p.partial = static_cast<float*>(
+      take(rows > kUnit ? sizeof(float) * 2 * nblk(rows, kUnit) * cols : 0));
+  p.bytes = off;
+  return p;
+}
+
+template <typename T, int V>
+cudaError_t fwd(int64_t rows, int64_t cols, int64_t vocab, float scale, const int* ids,
+                const void* table, void* y, cudaStream_t st) {
+  const int64_t nv = cols / V;
+  launch(embed_scaled_fwd_kernel<T, V>, dim3((unsigned)nblk(rows * nv, kFwdUnroll * kThreads)),
+         dim3(kThreads), 0, st, rows, (unsigned)nv, vocab, scale, ids,
+         static_cast<const T*>(table), static_cast<T*>(y));
+  return cudaGetLastError();
+}
+
+template <int V>
+cudaError_t accum(AccumArgs a, cudaStream_t st) {
+  const int64_t nv = nblk(a.cols, V);
+  a.group = 8;
+  while (a.group < kThreads && a.group < nv) a.group *= 2;
+  const int groups = kThreads / a.group;
+  const int64_t slabs = nblk(nv, a.group);
+  // positions per group: as many as leave every SM sixteen CTAs' worth of groups
+  const int64_t fill = (int64_t)sm_count() * 16 * groups;
+  a.window = (int)imax(1, imin(32, a.rows * slabs / fill));
+  a.acc_blocks = nblk(nblk(a.rows, a.window), groups);
+  int64_t clear = 0;
+  if (!a.accumulate) clear = imin(nblk(a.vocab, groups), (int64_t)sm_count() * 8);
+  launch(embed_accum_kernel<V>, dim3((unsigned)(a.acc_blocks + clear), (unsigned)slabs),
+         dim3(kThreads), 0, st, a);
+  if (a.rows > kUnit)
+    launch(embed_join_kernel<V>, dim3((unsigned)nblk(a.rows, kUnit), (unsigned)nblk(nv, 32)),
+           dim3(kThreads), 0, st, a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t embed_scaled_fwd(int64_t rows, int64_t cols, int64_t vocab, int dt, float scale,
                              const int* ids, const void* table, void* y, cudaStream_t st) {
-  if (dt == DT_BF16)
-    launch(embed_scaled_fwd_kernel<__nv_bfloat16>, dim3((unsigned)rows), dim3(256), 0, st, cols,
-           vocab, scale, ids, static_cast<const __nv_bfloat16*>(table),
-           static_cast<__nv_bfloat16*>(y));
-  else
-    launch(embed_scaled_fwd_kernel<float>, dim3((unsigned)rows), dim3(256), 0, st, cols, vocab,
-           scale, ids, static_cast<const float*>(table), static_cast<float*>(y));
-  return cudaGetLastError();
+  using bf16 = __nv_bfloat16;
+  const int v = vec_width(cols, dt == DT_BF16 ? 2 : 4);
+  if (dt == DT_BF16) {
+    switch (v) {
+      case 8: return fwd<bf16, 8>(rows, cols, vocab, scale, ids, table, y, st);
+      case 4: return fwd<bf16, 4>(rows, cols, vocab, scale, ids, table, y, st);
+      case 2: return fwd<bf16, 2>(rows, cols, vocab, scale, ids, table, y, st);
+      default: return fwd<bf16, 1>(rows, cols, vocab, scale, ids, table, y, st);
+    }
+  }
+  switch (v) {
+    case 4: return fwd<float, 4>(rows, cols, vocab, scale, ids, table, y, st);
+    case 2: return fwd<float, 2>(rows, cols, vocab, scale, ids, table, y, st);
+    default: return fwd<float, 1>(rows, cols, vocab, scale, ids, table, y, st);
+  }
 }
 
 size_t embed_scaled_bwd_ws_bytes(int64_t rows, int64_t cols, int64_t vocab) {
-  (void)cols;
-  (void)vocab;
-  return (size_t)rows * sizeof(int4);
+  return plan(nullptr, rows, cols, vocab).bytes;
 }
 
 cudaError_t embed_scaled_bwd(int64_t rows, int64_t cols, int64_t vocab, float scale,
                              const int* ids, const float* dy, float* d_table, int accumulate,
                              void* ws, cudaStream_t st) {
-  if (!accumulate) {
-    const cudaError_t e = cudaMemsetAsync(d_table, 0, sizeof(float) * (size_t)vocab * cols, st);
-    if (e != cudaSuccess) return e;
+  const Plan p = plan(ws, rows, cols, vocab);
+  unsigned char* present = accumulate ? nullptr : p.present;
+  int* n_valid = p.head;
+  if (rows <= kRankRows) {
+    if (present) {
+      const cudaError_t e = cudaMemsetAsync(present, 0, vocab, st);
+      if (e != cudaSuccess) return e;
+    }
+    launch(embed_rank_kernel, dim3((unsigned)nblk(rows, kRankPerCta)), dim3(kThreads), 0, st,
+           (int)rows, (int)vocab, ids, p.sorted, n_valid, present);
+  } else {
+    const int per_block = (int)deal_rows(rows);
+    const dim3 grid((unsigned)nblk(rows, per_block));
+    int* base = p.head + 1;
+    launch(embed_count_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block, (int)vocab,
+           ids, p.counts);
+    launch(embed_deal_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block, (int)vocab,
+           ids, (const int*)p.counts, p.dealt, base);
+    const int bins = (int)((vocab - 1) / kBuckets + 1);
+    int warps = kThreads / 32;      // as many histograms as 96 KB hold
+    while (warps > 1 && (size_t)bins * (warps + 2) * 4 > 96 * 1024) warps /= 2;
+    const size_t smem = sizeof(int) * (size_t)bins * (warps + 2);
+    if (smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(
+          embed_bucket_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+      if (e != cudaSuccess) return e;
+    }
+    launch(embed_bucket_kernel, dim3(kBuckets), dim3(kThreads), smem, st, (int)vocab, bins, warps,
+           (const int*)base, (const int2*)p.dealt, p.sorted, present);
+    n_valid = base + kBuckets;
   }
-  int4* sorted = static_cast<int4*>(ws);
-  launch(embed_rank_kernel, dim3(nblk(rows, kRankRows)), dim3(kRankThreads), 0, st, (int)rows,
-         (int)vocab, ids, sorted);
-  launch(embed_run_kernel, dim3((unsigned)rows), dim3(256), 0, st, cols, (int)vocab, scale,
-         (const int4*)sorted, dy, d_table);
-  return cudaGetLastError();
+  AccumArgs a;
+  a.cols = cols;
+  a.rows = (int)rows;
+  a.vocab = (int)vocab;
+  a.scale = scale;
+  a.accumulate = accumulate;
+  a.sorted = p.sorted;
+  a.n_valid = n_valid;
+  a.present = present;
+  a.dy = dy;
+  a.d_table = d_table;
+  a.partial = p.partial;
+  const int v = vec_width(cols, 4);
+  return v == 4 ? accum<4>(a, st) : v == 2 ? accum<2>(a, st) : accum<1>(a, st);
 }
 
 }  // namespace sbp

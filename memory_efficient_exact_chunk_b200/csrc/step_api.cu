@@ -39,15 +39,15 @@ sbp_status check_ws(void* ws, size_t have, size_t need) {
 }
 
 // ------------------------------------------------------------------------ embedding
-constexpr int64_t kMaxRows = (int64_t)1 << 30;
+constexpr int64_t kMaxRows = (int64_t)1 << 30, kMaxCols = (int64_t)1 << 20;
 
 sbp_status check_embed(int64_t rows, int64_t cols, int64_t vocab, int dt, const void* ids,
                        const void* a, const void* b) {
   if (rows <= 0 || cols <= 0 || vocab <= 0)
     return fail(SBP_ERR_INVALID_ARG, "rows, cols and vocab must be positive");
   if (dt != SBP_F32 && dt != SBP_BF16) return fail(SBP_ERR_INVALID_ARG, "unknown dtype %d", dt);
-  if (rows >= kMaxRows || cols >= kMaxRows)
-    return fail(SBP_ERR_UNSUPPORTED, "rows and cols must be below 2^30");
+  if (rows >= kMaxRows || cols > kMaxCols)
+    return fail(SBP_ERR_UNSUPPORTED, "rows must be below 2^30 and cols at most 2^20");
   if (vocab > kEmbedMaxVocab) return fail(SBP_ERR_UNSUPPORTED, "vocab must be at most 2^22");
   const void* ptrs[] = {ids, a, b};
   for (const void* p : ptrs)
@@ -155,7 +155,7 @@ sbp_status sbp_embedding_scaled_forward(int64_t rows, int64_t cols, int64_t voca
 }
 
 size_t sbp_embedding_scaled_backward_workspace_size(int64_t rows, int64_t cols, int64_t vocab) {
-  if (rows <= 0 || cols <= 0 || vocab <= 0 || rows >= kMaxRows || cols >= kMaxRows ||
+  if (rows <= 0 || cols <= 0 || vocab <= 0 || rows >= kMaxRows || cols > kMaxCols ||
       vocab > kEmbedMaxVocab)
     return 0;
   return embed_scaled_bwd_ws_bytes(rows, cols, vocab);
