@@ -66,7 +66,7 @@ embed_scaled_fwd_kernel(int64_t rows, unsigned nv, int64_t vocab, float scale,
 // What the accumulation reads of a sorted position: its row, and its run (the positions with the
 // same id): where it starts and how long it is, and the id.
 //   sorted[p] = {row, start, length, id},  p in [0, *n_valid); rows of ids outside [0, vocab)
-// are left out.  present[v] (where it is wanted) tells whether id v occurs.
+// are left out.
 
 // Few rows: the sorted position of every row by counting.  A run starts at the number of rows
 // with a smaller id, and a row stands behind the earlier rows of its own id.  Sixteen threads
@@ -76,7 +76,7 @@ constexpr int64_t kRankRows = 4096;
 constexpr int kRankShare = 16, kRankPerCta = kThreads / kRankShare;
 __global__ void __launch_bounds__(kThreads)
 embed_rank_kernel(int rows, int vocab, const int* __restrict__ ids, int4* __restrict__ sorted,
-                  int* __restrict__ n_valid, unsigned char* __restrict__ present) {
+                  int* __restrict__ n_valid) {
   __shared__ __align__(16) int key[kRankRows];
   for (int i = threadIdx.x; i < rows; i += kThreads) {
     const int v = ids[i];
@@ -100,10 +100,7 @@ embed_rank_kernel(int rows, int vocab, const int* __restrict__ ids, int4* __rest
     equal += __shfl_xor_sync(0xffffffffu, equal, o);
     before += __shfl_xor_sync(0xffffffffu, before, o);
   }
-  if (part == 0 && r < rows && mine < vocab) {
-    sorted[less + before] = make_int4(r, less, equal, mine);
-    if (present && before == 0) present[mine] = 1;
-  }
+  if (part == 0 && r < rows && mine < vocab) sorted[less + before] = make_int4(r, less, equal, mine);
   if (blockIdx.x == 0) {
     __shared__ int red[kThreads / 32];
     int n = 0;
@@ -224,7 +221,8 @@ embed_deal_kernel(int rows, int per_block, int vocab, const int* __restrict__ id
 }
 
 // One CTA per bucket: a counting sort by bin = id / kBuckets with `warps` histograms.  Shared
-// memory: hist[warps][bins], start[bins], len[bins].
+// memory: hist[warps][bins], start[bins], len[bins].  present[v] (where it is wanted) tells
+// whether id v occurs.
 __global__ void __launch_bounds__(kThreads)
 embed_bucket_kernel(int vocab, int bins, int warps, const int* __restrict__ base,
                     const int2* __restrict__ dealt, int4* __restrict__ sorted,
@@ -320,25 +318,67 @@ struct AccumArgs {
   int64_t acc_blocks;      // CTAs that accumulate; the ones behind them clear absent rows
   const int4* sorted;
   const int* n_valid;
+  const int* ids;          // the ids where they are few, else null:
   const unsigned char* present;
   const float* dy;
   float *d_table, *partial;
 };
 
+// CTA b of nb clears its share of the table rows whose id does not occur, by the flags of the
+// sort, or by marking the few ids in shared memory.
+constexpr int kClearRows = 4096;
+template <int V>
+__device__ void clear_absent(const AccumArgs& a, int64_t b, int64_t nb) {
+  __shared__ unsigned char here[kClearRows];
+  const int64_t nv = a.cols / V, per = (a.vocab + nb - 1) / nb;
+  const int64_t end = imin(a.vocab, (b + 1) * per);
+  const float zero[V] = {};
+  for (int64_t v0 = b * per; v0 < end; v0 += kClearRows) {
+    const int n = (int)imin(kClearRows, end - v0);
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads) here[i] = a.ids ? 0 : a.present[v0 + i];
+    if (a.ids) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < a.rows; i += kThreads) {
+        const int64_t v = a.ids[i] - v0;
+        if (v >= 0 && v < n) here[v] = 1;
+      }
+    }
+    __syncthreads();
+    // a warp per row: its lanes write the row's vectors side by side
+    for (int i = threadIdx.x / 32; i < n; i += kThreads / 32) {
+      if (here[i]) continue;
+      float* d = a.d_table + (v0 + i) * a.cols;
+      for (int64_t c = threadIdx.x % 32; c < nv; c += 32) vstore<V>(d + c * V, zero);
+    }
+  }
+}
+
+// d_table row v (+)= scale * sum
+template <int V>
+__device__ __forceinline__ void put_row(const AccumArgs& a, int v, int64_t c, float (&sum)[V]) {
+  float* d = a.d_table + (int64_t)v * a.cols + c;
+  if (a.accumulate) {
+    float old[V];
+    vload<V>(d, old);
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum[j] = fmaf(a.scale, sum[j], old[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum[j] *= a.scale;
+  }
+  vstore<V>(d, sum);
+}
+
 template <int V>
 __global__ void __launch_bounds__(kThreads)
 embed_accum_kernel(AccumArgs a) {
-  const int64_t c = ((int64_t)blockIdx.y * a.group + threadIdx.x % a.group) * V;
-  const int g = threadIdx.x / a.group, groups = kThreads / a.group;
   if ((int64_t)blockIdx.x >= a.acc_blocks) {
-    // table rows whose id does not occur
-    const int64_t stride = (int64_t)(gridDim.x - a.acc_blocks) * groups;
-    if (c >= a.cols) return;
-    const float zero[V] = {};
-    for (int64_t v = (blockIdx.x - a.acc_blocks) * groups + g; v < a.vocab; v += stride)
-      if (!a.present[v]) vstore<V>(a.d_table + v * a.cols + c, zero);
+    if (blockIdx.y == 0) clear_absent<V>(a, blockIdx.x - a.acc_blocks, gridDim.x - a.acc_blocks);
     return;
   }
+  const int64_t c = ((int64_t)blockIdx.y * a.group + threadIdx.x % a.group) * V;
+  const int g = threadIdx.x / a.group, groups = kThreads / a.group;
   const int n = *a.n_valid;
   const int64_t p0 = ((int64_t)blockIdx.x * groups + g) * a.window;
   const int p1 = (int)imin(n, p0 + a.window);
@@ -368,20 +408,57 @@ embed_accum_kernel(AccumArgs a) {
     if (s.z > kUnit) {
       const int64_t slot = 2 * (int64_t)(p / kUnit) + (p == s.y);
       vstore<V>(a.partial + slot * a.cols + c, sum);
-      continue;
-    }
-    float* d = a.d_table + (int64_t)s.w * a.cols + c;
-    if (a.accumulate) {
-      float old[V];
-      vload<V>(d, old);
-#pragma unroll
-      for (int j = 0; j < V; ++j) sum[j] = fmaf(a.scale, sum[j], old[j]);
     } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) sum[j] *= a.scale;
+      put_row<V>(a, s.w, c, sum);
     }
-    vstore<V>(d, sum);
   }
+}
+
+// At most kFewRows rows: no sort.  A warp takes (row, 32 V columns); it marks the rows of the
+// same id by ballots over all ids and, where its own row is the first of them, adds them in
+// order.  One launch, where the sorted form takes three.
+constexpr int kFewRows = 256;
+template <int V>
+__global__ void __launch_bounds__(kThreads)
+embed_few_kernel(AccumArgs a, int slabs) {
+  if ((int64_t)blockIdx.x >= a.acc_blocks) {
+    clear_absent<V>(a, blockIdx.x - a.acc_blocks, gridDim.x - a.acc_blocks);
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  const int64_t item = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t r = item / slabs, c = ((item - r * slabs) * 32 + lane) * V;
+  if (r >= a.rows) return;
+  const int mine = a.ids[r];
+  if (!valid_id(mine, a.vocab)) return;
+  unsigned same[kFewRows / 32];
+#pragma unroll
+  for (int q = 0; q < kFewRows / 32; ++q) {
+    const int i = q * 32 + lane;
+    same[q] = __ballot_sync(0xffffffffu, i < a.rows && a.ids[i] == mine);
+    // an earlier row has this id: that row's warp adds it
+    if (q * 32 < r && (same[q] & (r >= q * 32 + 32 ? ~0u : (1u << (r & 31)) - 1))) return;
+  }
+  if (c >= a.cols) return;
+  float sum[V] = {};
+#pragma unroll
+  for (int q = 0; q < kFewRows / 32; ++q) {
+    const float* dy = a.dy + q * 32 * a.cols + c;
+    unsigned m = same[q];
+    while (m) {
+      float x[4][V] = {};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (m) vload<V>(dy + (int64_t)(__ffs(m) - 1) * a.cols, x[k]);
+        m &= m - 1;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum[j] += x[k][j];
+    }
+  }
+  put_row<V>(a, mine, c, sum);
 }
 
 // Runs longer than kUnit.  CTA x looks for the run that starts in positions [x kUnit, (x + 1)
@@ -427,22 +504,12 @@ embed_join_kernel(AccumArgs a) {
   for (int w = 1; w < kThreads / 32; ++w)
 #pragma unroll
     for (int j = 0; j < V; ++j) sum[j] += sums[w][lane * V + j];
-  float* d = a.d_table + (int64_t)s.w * a.cols + c;
-  if (a.accumulate) {
-    float old[V];
-    vload<V>(d, old);
-#pragma unroll
-    for (int j = 0; j < V; ++j) sum[j] = fmaf(a.scale, sum[j], old[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) sum[j] *= a.scale;
-  }
-  vstore<V>(d, sum);
+  put_row<V>(a, s.w, c, sum);
 }
 
 // ---------------------------------------------------------------- workspace
 struct Plan {
-  int* head;                // number of valid rows, then the buckets' starts
+  int* head;                // number of valid rows, or the buckets' starts with it behind them
   int4* sorted;
   unsigned char* present;
   int2* dealt;
@@ -464,10 +531,10 @@ Plan plan(void* ws, int64_t rows, int64_t cols, int64_t vocab) {
     off += (n + 255) & ~size_t(255);
     return q;
   };
-  p.head = static_cast<int*>(take(sizeof(int) * (1 + kBuckets + 1)));
+  p.head = static_cast<int*>(take(sizeof(int) * (kBuckets + 1)));
   p.sorted = static_cast<int4*>(take(sizeof(int4) * rows));
-  p.present = static_cast<unsigned char*>(take(vocab));
   const bool deal = rows > kRankRows;
+  p.present = static_cast<unsigned char*>(take(deal ? vocab : 0));
   p.dealt = static_cast<int2*>(take(deal ? sizeof(int2) * rows : 0));
   p.counts =
       static_cast<int*>(take(deal ? sizeof(int) * kBuckets * nblk(rows, deal_rows(rows)) : 0));
@@ -487,9 +554,23 @@ cudaError_t fwd(int64_t rows, int64_t cols, int64_t vocab, float scale, const in
   return cudaGetLastError();
 }
 
+// CTAs that clear absent rows
+int64_t clear_blocks(const AccumArgs& a) {
+  return a.accumulate ? 0 : imin(nblk(a.vocab, kThreads / 32), (int64_t)sm_count() * 8);
+}
+
+template <int V>
+cudaError_t accum_few(AccumArgs a, cudaStream_t st) {
+  const int64_t slabs = nblk(a.cols, 32 * V);
+  a.acc_blocks = nblk(a.rows * slabs, kThreads / 32);
+  launch(embed_few_kernel<V>, dim3((unsigned)(a.acc_blocks + clear_blocks(a))), dim3(kThreads), 0,
+         st, a, (int)slabs);
+  return cudaGetLastError();
+}
+
 template <int V>
 cudaError_t accum(AccumArgs a, cudaStream_t st) {
-  const int64_t nv = nblk(a.cols, V);
+  const int64_t nv = a.cols / V;
   a.group = 8;
   while (a.group < kThreads && a.group < nv) a.group *= 2;
   const int groups = kThreads / a.group;
@@ -498,13 +579,46 @@ cudaError_t accum(AccumArgs a, cudaStream_t st) {
   const int64_t fill = (int64_t)sm_count() * 16 * groups;
   a.window = (int)imax(1, imin(32, a.rows * slabs / fill));
   a.acc_blocks = nblk(nblk(a.rows, a.window), groups);
-  int64_t clear = 0;
-  if (!a.accumulate) clear = imin(nblk(a.vocab, groups), (int64_t)sm_count() * 8);
-  launch(embed_accum_kernel<V>, dim3((unsigned)(a.acc_blocks + clear), (unsigned)slabs),
+  launch(embed_accum_kernel<V>,
+         dim3((unsigned)(a.acc_blocks + clear_blocks(a)), (unsigned)slabs), dim3(kThreads), 0, st,
+         a);
+  launch(embed_join_kernel<V>, dim3((unsigned)nblk(a.rows, kUnit), (unsigned)nblk(nv, 32)),
          dim3(kThreads), 0, st, a);
-  if (a.rows > kUnit)
-    launch(embed_join_kernel<V>, dim3((unsigned)nblk(a.rows, kUnit), (unsigned)nblk(nv, 32)),
-           dim3(kThreads), 0, st, a);
+  return cudaGetLastError();
+}
+
+// sorted, n_valid, and what tells the absent ids
+cudaError_t sort_by_id(int64_t rows, int64_t vocab, const int* ids, const Plan& p, AccumArgs& a,
+                       cudaStream_t st) {
+  a.sorted = p.sorted;
+  a.n_valid = p.head;
+  if (rows <= kRankRows) {
+    launch(embed_rank_kernel, dim3((unsigned)nblk(rows, kRankPerCta)), dim3(kThreads), 0, st,
+           (int)rows, (int)vocab, ids, p.sorted, p.head);
+    return cudaGetLastError();
+  }
+  const int per_block = (int)deal_rows(rows);
+  const dim3 grid((unsigned)nblk(rows, per_block));
+  int* base = p.head;
+  launch(embed_count_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block, (int)vocab,
+         ids, p.counts);
+  launch(embed_deal_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block, (int)vocab,
+         ids, (const int*)p.counts, p.dealt, base);
+  const int bins = (int)((vocab - 1) / kBuckets + 1);
+  int warps = kThreads / 32;      // as many histograms as 96 KB hold
+  while (warps > 1 && (size_t)bins * (warps + 2) * 4 > 96 * 1024) warps /= 2;
+  const size_t smem = sizeof(int) * (size_t)bins * (warps + 2);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        embed_bucket_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+    if (e != cudaSuccess) return e;
+  }
+  launch(embed_bucket_kernel, dim3(kBuckets), dim3(kThreads), smem, st, (int)vocab, bins, warps,
+         (const int*)base, (const int2*)p.dealt, p.sorted,
+         a.accumulate ? static_cast<unsigned char*>(nullptr) : p.present);
+  a.n_valid = base + kBuckets;
+  a.ids = nullptr;
+  a.present = p.present;
   return cudaGetLastError();
 }
 
@@ -537,49 +651,21 @@ cudaError_t embed_scaled_bwd(int64_t rows, int64_t cols, int64_t vocab, float sc
                              const int* ids, const float* dy, float* d_table, int accumulate,
                              void* ws, cudaStream_t st) {
   const Plan p = plan(ws, rows, cols, vocab);
-  unsigned char* present = accumulate ? nullptr : p.present;
-  int* n_valid = p.head;
-  if (rows <= kRankRows) {
-    if (present) {
-      const cudaError_t e = cudaMemsetAsync(present, 0, vocab, st);
-      if (e != cudaSuccess) return e;
-    }
-    launch(embed_rank_kernel, dim3((unsigned)nblk(rows, kRankPerCta)), dim3(kThreads), 0, st,
-           (int)rows, (int)vocab, ids, p.sorted, n_valid, present);
-  } else {
-    const int per_block = (int)deal_rows(rows);
-    const dim3 grid((unsigned)nblk(rows, per_block));
-    int* base = p.head + 1;
-    launch(embed_count_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block, (int)vocab,
-           ids, p.counts);
-    launch(embed_deal_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block, (int)vocab,
-           ids, (const int*)p.counts, p.dealt, base);
-    const int bins = (int)((vocab - 1) / kBuckets + 1);
-    int warps = kThreads / 32;      // as many histograms as 96 KB hold
-    while (warps > 1 && (size_t)bins * (warps + 2) * 4 > 96 * 1024) warps /= 2;
-    const size_t smem = sizeof(int) * (size_t)bins * (warps + 2);
-    if (smem > 48 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(
-          embed_bucket_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
-      if (e != cudaSuccess) return e;
-    }
-    launch(embed_bucket_kernel, dim3(kBuckets), dim3(kThreads), smem, st, (int)vocab, bins, warps,
-           (const int*)base, (const int2*)p.dealt, p.sorted, present);
-    n_valid = base + kBuckets;
-  }
-  AccumArgs a;
+  AccumArgs a = {};
   a.cols = cols;
   a.rows = (int)rows;
   a.vocab = (int)vocab;
   a.scale = scale;
   a.accumulate = accumulate;
-  a.sorted = p.sorted;
-  a.n_valid = n_valid;
-  a.present = present;
+  a.ids = ids;
   a.dy = dy;
   a.d_table = d_table;
   a.partial = p.partial;
   const int v = vec_width(cols, 4);
+  if (rows <= kFewRows)
+    return v == 4 ? accum_few<4>(a, st) : v == 2 ? accum_few<2>(a, st) : accum_few<1>(a, st);
+  const cudaError_t e = sort_by_id(rows, vocab, ids, p, a, st);
+  if (e != cudaSuccess) return e;
   return v == 4 ? accum<4>(a, st) : v == 2 ? accum<2>(a, st) : accum<1>(a, st);
 }
 

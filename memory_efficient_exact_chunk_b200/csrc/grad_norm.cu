@@ -6,8 +6,12 @@
 // Products and sums are formed in 64 bits: the square of an fp32 value neither overflows nor
 // vanishes there.  Both passes are bound by HBM (4 bytes read per element, then 8 moved where
 // the clipping bites).  The tensors' pointers travel as kernel parameters, so a call copies
-// nothing to the device and can be captured; tensors are cut into chunks of kChunk elements.
-#include <cmath>
+// nothing to the device and can be captured.
+//
+// The tensors are one list of units of four elements (the last unit of a tensor may hold fewer).
+// Every CTA takes an equal contiguous range of it, and inside a range every thread its own units,
+// so that many small and few large tensors load the GPU alike.
+#include <cooperative_groups.h>
 
 #include "sbp_internal.cuh"
 
@@ -15,37 +19,67 @@ namespace sbp {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int64_t kChunk = 16384;        // elements of a chunk
-constexpr int kMaxTensors = 256;         // tensors of one launch
-constexpr int kBlocksPerSm = 8;
+namespace cg = cooperative_groups;
 
+constexpr int kThreads = 256;
+constexpr int kBlocksPerSm = 8;
+constexpr int64_t kUnitsPerBlock = 4 * kThreads;   // a CTA's range is at least this long
+// tensors of one launch: the small table where it is enough, as a launch copies its parameters
+constexpr int kSmallTable = 64, kLargeTable = 1024;
+
+template <int N>
 struct Tensors {
   int n;
-  int64_t chunks;                        // first[n]
-  const float* src[kMaxTensors];
-  float* dst[kMaxTensors];
-  int64_t numel[kMaxTensors];
-  int64_t first[kMaxTensors + 1];        // chunk index at which each tensor begins
+  int64_t units;          // of all n tensors
+  int64_t end[N];         // units up to and including tensor i, times 4, plus the number of
+                          // elements that its last unit lacks
+  const float* src[N];
+  float* dst[N];
 };
 
-// the tensor that chunk c belongs to: the last one with first[i] <= c
-__device__ __forceinline__ int tensor_of(const Tensors& t, int64_t c) {
-  int lo = 0, hi = t.n;
-  while (hi - lo > 1) {
+// the tensor in [lo, n) that unit u belongs to, by the table of ends
+__device__ __forceinline__ int tensor_of(const int64_t* end, int lo, int n, int64_t u) {
+  int hi = n - 1;
+  while (lo < hi) {
     const int mid = (lo + hi) / 2;
-    if (t.first[mid] <= c)
-      lo = mid;
+    if ((end[mid] >> 2) <= u)
+      lo = mid + 1;
     else
       hi = mid;
   }
   return lo;
 }
 
-__device__ __forceinline__ double block_sum(double v, double* red) {
+// One unit: where its elements are and how many it has.
+struct Unit {
+  int64_t at;       // element index in the tensor
+  int have;
+  __device__ __forceinline__ Unit(const int64_t* end, int i, int64_t u)
+      : at(4 * (u - (i ? end[i - 1] >> 2 : 0))),
+        have(u == (end[i] >> 2) - 1 ? 4 - (int)(end[i] & 3) : 4) {}
+};
+__device__ __forceinline__ float4 load_unit(const float* p, int have) {
+  if (have == 4) return *reinterpret_cast<const float4*>(p);
+  return make_float4(p[0], have > 1 ? p[1] : 0.f, have > 2 ? p[2] : 0.f, 0.f);
+}
+__device__ __forceinline__ void store_unit(float* p, int have, float4 v) {
+  if (have == 4) {
+    *reinterpret_cast<float4*>(p) = v;
+    return;
+  }
+  p[0] = v.x;
+  if (have > 1) p[1] = v.y;
+  if (have > 2) p[2] = v.z;
+}
+
+__device__ __forceinline__ double warp_sum64(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
+  return v;
+}
+
+__device__ __forceinline__ double block_sum(double v, double* red) {
+  v = warp_sum64(v);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   double s = 0.0;
@@ -54,34 +88,8 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
 }
 
 __device__ __forceinline__ double square(float v) { return (double)v * (double)v; }
-
-__global__ void __launch_bounds__(kThreads)
-sqsum_kernel(const __grid_constant__ Tensors t, double* __restrict__ partial) {
-  __shared__ double red[32];
-  double s = 0.0;
-  for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    const int i = tensor_of(t, c);
-    const int64_t o = (c - t.first[i]) * kChunk;
-    const int n = (int)imin(kChunk, t.numel[i] - o);
-    const float* g = t.src[i] + o;
-    const float4* g4 = reinterpret_cast<const float4*>(g);
-    for (int k = threadIdx.x; k < n / 4; k += kThreads) {
-      const float4 v = g4[k];
-      s += square(v.x) + square(v.y) + (square(v.z) + square(v.w));
-    }
-    for (int k = n / 4 * 4 + threadIdx.x; k < n; k += kThreads) s += square(g[k]);
-  }
-  s = block_sum(s, red);
-  if (threadIdx.x == 0) partial[blockIdx.x] = s;
-}
-
-__global__ void __launch_bounds__(kThreads)
-sqsum_finish_kernel(int64_t n, const double* __restrict__ partial, double* __restrict__ sqsum) {
-  __shared__ double red[32];
-  double s = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += kThreads) s += partial[i];
-  s = block_sum(s, red);
-  if (threadIdx.x == 0) *sqsum = s;
+__device__ __forceinline__ double square(float4 v) {
+  return square(v.x) + square(v.y) + (square(v.z) + square(v.w));
 }
 
 // coefficient of the clipping; 1 where the norm is not finite (no right one exists)
@@ -91,87 +99,269 @@ __device__ __forceinline__ float clip_coef(double norm, float max_norm) {
   return c < 1.0 ? (float)c : 1.f;
 }
 
+// [u0, u1): CTA b's units
+template <int N>
+__device__ __forceinline__ void my_range(const Tensors<N>& t, int64_t& u0, int64_t& u1) {
+  const int64_t per = (t.units + gridDim.x - 1) / gridDim.x;
+  u0 = imin(t.units, blockIdx.x * per);
+  u1 = imin(t.units, u0 + per);
+}
+
+// The units [c, c + kUnitsPerBlock) of a range that all lie in tensor i and are whole take the
+// direct path; a piece with a tensor's border or last unit looks each unit's tensor up.
+template <int N>
+__device__ __forceinline__ bool direct(const Tensors<N>& t, int i, int64_t c, int64_t u1) {
+  return c + kUnitsPerBlock <= imin(u1, (t.end[i] >> 2) - 1);
+}
+
+template <int N>
 __global__ void __launch_bounds__(kThreads)
-clip_kernel(const __grid_constant__ Tensors t, const double* __restrict__ sqsum, float max_norm,
-            float* __restrict__ norm_out) {
-  const double norm = sqrt(*sqsum);
+sqsum_kernel(const __grid_constant__ Tensors<N> t, double* __restrict__ partial) {
+  __shared__ double red[kThreads / 32];
+  int64_t u0, u1;
+  my_range(t, u0, u1);
+  double s[4] = {};
+  int i = 0;
+  for (int64_t c = u0; c < u1; c += kUnitsPerBlock) {
+    if (c == u0 || (t.end[i] >> 2) <= c) i = tensor_of(t.end, i, t.n, c);
+    float4 v[4];
+    if (direct(t, i, c, u1)) {
+      const float4* g = reinterpret_cast<const float4*>(t.src[i]) +
+                        (c - (i ? t.end[i - 1] >> 2 : 0)) + threadIdx.x;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = g[k * kThreads];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t u = c + threadIdx.x + k * kThreads;
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (u >= u1) continue;
+        const int j = tensor_of(t.end, i, t.n, u);
+        const Unit x(t.end, j, u);
+        v[k] = load_unit(t.src[j] + x.at, x.have);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[k] += square(v[k]);
+  }
+  const double v = block_sum((s[0] + s[1]) + (s[2] + s[3]), red);
+  if (threadIdx.x == 0) partial[blockIdx.x] = v;
+}
+
+// sum of the partial sums, the same bits in every CTA
+__device__ __forceinline__ double join(int64_t n, const double* __restrict__ partial,
+                                       double* red) {
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < n; i += kThreads) s += partial[i];
+  return block_sum(s, red);
+}
+
+__global__ void __launch_bounds__(kThreads)
+sqsum_finish_kernel(int64_t n, const double* __restrict__ partial, double* __restrict__ sqsum) {
+  __shared__ double red[kThreads / 32];
+  const double s = join(n, partial, red);
+  if (threadIdx.x == 0) *sqsum = s;
+}
+
+__device__ __forceinline__ float4 scaled(float4 v, float c) {
+  return make_float4(v.x * c, v.y * c, v.z * c, v.w * c);
+}
+
+// A CTA walks its range from the end: what it read last while summing is still in L2.
+template <int N>
+__global__ void __launch_bounds__(kThreads)
+clip_kernel(const __grid_constant__ Tensors<N> t, int64_t parts,
+            const double* __restrict__ partial, float max_norm, float* __restrict__ norm_out) {
+  __shared__ double red[kThreads / 32];
+  const double norm = sqrt(join(parts, partial, red));
   const float coef = clip_coef(norm, max_norm);
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
-  for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    const int i = tensor_of(t, c);
-    const int64_t o = (c - t.first[i]) * kChunk;
-    const int n = (int)imin(kChunk, t.numel[i] - o);
-    const float* g = t.src[i] + o;
-    float* d = t.dst[i] + o;
-    if (g == d && coef == 1.f) continue;
-    const float4* g4 = reinterpret_cast<const float4*>(g);
-    float4* d4 = reinterpret_cast<float4*>(d);
-    for (int k = threadIdx.x; k < n / 4; k += kThreads) {
-      float4 v = g4[k];
-      v.x *= coef; v.y *= coef; v.z *= coef; v.w *= coef;
-      d4[k] = v;
+  int64_t u0, u1;
+  my_range(t, u0, u1);
+  for (int64_t p = (u1 - u0 - 1) / kUnitsPerBlock; u0 < u1 && p >= 0; --p) {
+    const int64_t c = u0 + p * kUnitsPerBlock;
+    const int i = tensor_of(t.end, 0, t.n, c);
+    if (direct(t, i, c, u1)) {
+      if (t.dst[i] == t.src[i] && coef == 1.f) continue;
+      const int64_t o = c - (i ? t.end[i - 1] >> 2 : 0) + threadIdx.x;
+      const float4* g = reinterpret_cast<const float4*>(t.src[i]) + o;
+      float4* d = reinterpret_cast<float4*>(t.dst[i]) + o;
+      float4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = g[k * kThreads];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) d[k * kThreads] = scaled(v[k], coef);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t u = c + threadIdx.x + k * kThreads;
+        if (u >= u1) continue;
+        const int j = tensor_of(t.end, i, t.n, u);
+        if (t.dst[j] == t.src[j] && coef == 1.f) continue;
+        const Unit x(t.end, j, u);
+        store_unit(t.dst[j] + x.at, x.have, scaled(load_unit(t.src[j] + x.at, x.have), coef));
+      }
     }
-    for (int k = n / 4 * 4 + threadIdx.x; k < n; k += kThreads) d[k] = g[k] * coef;
   }
 }
 
-// the next launch's tensors: up to kMaxTensors non-empty ones from index i on
-int64_t take(Tensors& t, int64_t i, int64_t n, const float* const* grads, float* const* outs,
-             const int64_t* numel) {
+// Few elements: one cluster holds them in registers, joins its CTAs' sums over distributed
+// shared memory and writes, in a single launch and with every element read once.
+constexpr int kFewCtas = 8, kFewThreads = 1024, kFewUnits = 4;
+constexpr int64_t kFewMax = (int64_t)kFewCtas * kFewThreads * kFewUnits;
+template <int N>
+__global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads)
+clip_few_kernel(const __grid_constant__ Tensors<N> t, float max_norm,
+                float* __restrict__ norm_out) {
+  __shared__ double red[kFewThreads / 32], sum;
+  __shared__ int64_t end[N];
+  cg::cluster_group cluster = cg::this_cluster();
+  for (int i = threadIdx.x; i < t.n; i += kFewThreads) end[i] = t.end[i];
+  __syncthreads();
+  float4 v[kFewUnits];
+  const float* src[kFewUnits];
+  float* dst[kFewUnits];
+  int have[kFewUnits];      // elements of the unit, 0 behind the last one
+  double s = 0.0;
+#pragma unroll
+  for (int k = 0; k < kFewUnits; ++k) {
+    const int64_t u = blockIdx.x * kFewThreads + threadIdx.x + k * (kFewCtas * kFewThreads);
+    have[k] = 0;
+    if (u >= t.units) continue;
+    const int i = tensor_of(end, 0, t.n, u);
+    const Unit x(end, i, u);
+    src[k] = t.src[i] + x.at;
+    dst[k] = t.dst[i] + x.at;
+    have[k] = x.have;
+    v[k] = load_unit(src[k], x.have);
+    s += square(v[k]);
+  }
+  s = block_sum(s, red);
+  if (threadIdx.x == 0) sum = s;
+  cluster.sync();
+  s = 0.0;
+#pragma unroll
+  for (int c = 0; c < kFewCtas; ++c) s += *cluster.map_shared_rank(&sum, c);
+  cluster.sync();           // no CTA ends while another reads its sum
+  const double norm = sqrt(s);
+  const float coef = clip_coef(norm, max_norm);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
+#pragma unroll
+  for (int k = 0; k < kFewUnits; ++k)
+    if (have[k] > 0 && (dst[k] != src[k] || coef != 1.f))
+      store_unit(dst[k], have[k], scaled(v[k], coef));
+}
+
+// the next launch's tensors: up to N non-empty ones from index i on
+template <int N>
+int64_t take(Tensors<N>& t, int64_t i, const GradTensors& g) {
   t.n = 0;
-  t.chunks = 0;
-  for (; i < n && t.n < kMaxTensors; ++i) {
-    if (numel[i] == 0) continue;
-    t.src[t.n] = grads[i];
-    t.dst[t.n] = outs ? outs[i] : const_cast<float*>(grads[i]);
-    t.numel[t.n] = numel[i];
-    t.first[t.n] = t.chunks;
-    t.chunks += (numel[i] + kChunk - 1) / kChunk;
+  t.units = 0;
+  for (; i < g.n && t.n < N; ++i) {
+    const int64_t m = g.numel[i];
+    if (m == 0) continue;
+    t.units += (m + 3) / 4;
+    t.src[t.n] = g.src[i];
+    t.dst[t.n] = g.dst ? g.dst[i] : const_cast<float*>(g.src[i]);
+    t.end[t.n] = 4 * t.units + (4 - m % 4) % 4;
     ++t.n;
   }
-  t.first[t.n] = t.chunks;
   return i;
 }
 
-unsigned grid_of(const Tensors& t) {
-  return (unsigned)imin(t.chunks, (int64_t)sm_count() * kBlocksPerSm);
+unsigned grid_of(int64_t units) {
+  return (unsigned)imax(1, imin((units + kUnitsPerBlock - 1) / kUnitsPerBlock,
+                                (int64_t)sm_count() * kBlocksPerSm));
+}
+
+template <int N>
+int64_t launch_sqsum(const GradTensors& g, double* partial, cudaStream_t st) {
+  int64_t parts = 0;
+  Tensors<N> t;
+  for (int64_t i = 0; i < g.n;) {
+    i = take(t, i, g);
+    if (t.n == 0) break;
+    const unsigned grid = grid_of(t.units);
+    launch(sqsum_kernel<N>, dim3(grid), dim3(kThreads), 0, st, t, partial + parts);
+    parts += grid;
+  }
+  return parts;
+}
+
+template <int N>
+void launch_clip(const GradTensors& g, int64_t parts, const double* partial, float max_norm,
+                 float* norm_out, cudaStream_t st) {
+  Tensors<N> t;
+  for (int64_t i = 0; i == 0 || i < g.n;) {     // one launch at least: it writes the norm
+    i = imax(1, take(t, i, g));
+    launch(clip_kernel<N>, dim3(grid_of(t.units)), dim3(kThreads), 0, st, t, parts, partial,
+           max_norm, norm_out);
+    norm_out = nullptr;
+  }
+}
+
+template <int N>
+void launch_few(const GradTensors& g, float max_norm, float* norm_out, cudaStream_t st) {
+  Tensors<N> t;
+  take(t, 0, g);
+  launch(clip_few_kernel<N>, dim3(kFewCtas), dim3(kFewThreads), 0, st, t, max_norm, norm_out);
+}
+
+constexpr size_t kPartialOffset = 256;
+
+double* partials(void* ws) {
+  return reinterpret_cast<double*>(static_cast<char*>(ws) + kPartialOffset);
+}
+
+int64_t sqsum_parts(const GradTensors& g, void* ws, cudaStream_t st) {
+  return g.n <= kSmallTable ? launch_sqsum<kSmallTable>(g, partials(ws), st)
+                            : launch_sqsum<kLargeTable>(g, partials(ws), st);
+}
+
+void clip_parts(const GradTensors& g, int64_t parts, const double* partial, float max_norm,
+                float* norm_out, cudaStream_t st) {
+  if (g.n <= kSmallTable)
+    launch_clip<kSmallTable>(g, parts, partial, max_norm, norm_out, st);
+  else
+    launch_clip<kLargeTable>(g, parts, partial, max_norm, norm_out, st);
 }
 
 }  // namespace
 
 size_t grad_norm_ws_bytes(int64_t n) {
-  const int64_t launches = n > 0 ? (n + kMaxTensors - 1) / kMaxTensors : 1;
-  return 256 + sizeof(double) * (size_t)(launches * sm_count() * kBlocksPerSm);
+  const int64_t launches = n / kLargeTable + 1;
+  return kPartialOffset + sizeof(double) * (size_t)(launches * sm_count() * kBlocksPerSm);
 }
 
-cudaError_t grad_sqsum(int64_t n, const float* const* grads, const int64_t* numel, double* sqsum,
-                       void* ws, cudaStream_t st) {
-  double* partial = reinterpret_cast<double*>(static_cast<char*>(ws) + 256);
-  int64_t parts = 0;
-  Tensors t;
-  for (int64_t i = 0; i < n;) {
-    i = take(t, i, n, grads, nullptr, numel);
-    if (t.n == 0) break;
-    launch(sqsum_kernel, dim3(grid_of(t)), dim3(kThreads), 0, st, t, partial + parts);
-    parts += grid_of(t);
-  }
-  launch(sqsum_finish_kernel, dim3(1), dim3(kThreads), 0, st, parts, (const double*)partial,
-         sqsum);
+cudaError_t grad_sqsum(const GradTensors& g, double* sqsum, void* ws, cudaStream_t st) {
+  const int64_t parts = sqsum_parts(g, ws, st);
+  launch(sqsum_finish_kernel, dim3(1), dim3(kThreads), 0, st, parts,
+         (const double*)partials(ws), sqsum);
   return cudaGetLastError();
 }
 
-cudaError_t grad_clip(int64_t n, const float* const* grads, float* const* outs,
-                      const int64_t* numel, const double* sqsum, float max_norm, float* norm_out,
+cudaError_t grad_clip(const GradTensors& g, const double* sqsum, float max_norm, float* norm_out,
                       cudaStream_t st) {
-  Tensors t;
-  bool first = true;
-  for (int64_t i = 0; first || i < n;) {
-    i = take(t, i, n, grads, outs, numel);
-    if (t.n == 0 && !first) break;
-    launch(clip_kernel, dim3(t.n ? grid_of(t) : 1u), dim3(kThreads), 0, st, t, sqsum, max_norm,
-           first ? norm_out : static_cast<float*>(nullptr));
-    first = false;
+  clip_parts(g, 1, sqsum, max_norm, norm_out, st);
+  return cudaGetLastError();
+}
+
+cudaError_t grad_clip_norm(const GradTensors& g, float max_norm, float* norm_out, void* ws,
+                           cudaStream_t st) {
+  int64_t units = 0, n = 0;
+  for (int64_t i = 0; i < g.n; ++i) {
+    units += (g.numel[i] + 3) / 4;
+    n += g.numel[i] > 0;
   }
+  if (units <= kFewMax && n <= kLargeTable) {
+    if (n <= kSmallTable)
+      launch_few<kSmallTable>(g, max_norm, norm_out, st);
+    else
+      launch_few<kLargeTable>(g, max_norm, norm_out, st);
+    return cudaGetLastError();
+  }
+  const int64_t parts = sqsum_parts(g, ws, st);
+  clip_parts(g, parts, partials(ws), max_norm, norm_out, st);
   return cudaGetLastError();
 }
 

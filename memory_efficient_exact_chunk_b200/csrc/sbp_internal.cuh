@@ -398,12 +398,18 @@ size_t qk_norm_bwd_partial_floats(int64_t rows, int64_t n_heads, int64_t n_kv, i
 cudaError_t qk_norm_rope_bwd(const QkNorm& a, float* dq_g, float* dk_g, float* partial,
                              cudaStream_t st);
 
-// global gradient norm and clipping (grad_norm.cu); host arrays of device pointers
+// global gradient norm and clipping (grad_norm.cu)
+struct GradTensors {          // host arrays of n entries
+  int64_t n = 0;
+  const float* const* src = nullptr;   // device pointers, 16-byte aligned
+  float* const* dst = nullptr;         // null: in place
+  const int64_t* numel = nullptr;
+};
 size_t grad_norm_ws_bytes(int64_t n);
-cudaError_t grad_sqsum(int64_t n, const float* const* grads, const int64_t* numel, double* sqsum,
-                       void* ws, cudaStream_t st);
-cudaError_t grad_clip(int64_t n, const float* const* grads, float* const* outs,
-                      const int64_t* numel, const double* sqsum, float max_norm, float* norm_out,
+cudaError_t grad_sqsum(const GradTensors& g, double* sqsum, void* ws, cudaStream_t st);
+cudaError_t grad_clip(const GradTensors& g, const double* sqsum, float max_norm, float* norm_out,
                       cudaStream_t st);
+cudaError_t grad_clip_norm(const GradTensors& g, float max_norm, float* norm_out, void* ws,
+                           cudaStream_t st);
 
 }  // namespace sbp

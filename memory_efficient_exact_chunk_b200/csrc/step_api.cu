@@ -136,6 +136,16 @@ sbp_status check_grads(int64_t n, const float* const* grads, float* const* outs,
   return SBP_OK;
 }
 
+GradTensors tensors_of(int64_t n, const float* const* grads, float* const* outs,
+                       const int64_t* numel) {
+  GradTensors g;
+  g.n = n;
+  g.src = grads;
+  g.dst = outs;
+  g.numel = numel;
+  return g;
+}
+
 sbp_status check_max_norm(float max_norm) {
   if (!(max_norm >= 0.f)) return fail(SBP_ERR_INVALID_ARG, "max_norm must be >= 0");
   return SBP_OK;
@@ -254,7 +264,8 @@ sbp_status sbp_grad_sqsum(int64_t n, const float* const* grads, const int64_t* n
   if (sbp_status s = check_grads(n, grads, nullptr, numel)) return s;
   if (!sqsum || !aligned(sqsum, 8)) return fail(SBP_ERR_INVALID_ARG, "sqsum NULL or misaligned");
   if (sbp_status s = check_ws(workspace, workspace_bytes, grad_norm_ws_bytes(n))) return s;
-  STEP_CK(grad_sqsum(n, grads, numel, sqsum, workspace, static_cast<cudaStream_t>(stream)));
+  STEP_CK(grad_sqsum(tensors_of(n, grads, nullptr, numel), sqsum, workspace,
+                     static_cast<cudaStream_t>(stream)));
   return SBP_OK;
 }
 
@@ -265,7 +276,7 @@ sbp_status sbp_grad_clip(int64_t n, const float* const* grads, float* const* out
   if (!sqsum || !aligned(sqsum, 8)) return fail(SBP_ERR_INVALID_ARG, "sqsum NULL or misaligned");
   if (sbp_status s = check_max_norm(max_norm)) return s;
   if (!aligned(norm_out, 4)) return fail(SBP_ERR_INVALID_ARG, "norm_out is misaligned");
-  STEP_CK(grad_clip(n, grads, outs, numel, sqsum, max_norm, norm_out,
+  STEP_CK(grad_clip(tensors_of(n, grads, outs, numel), sqsum, max_norm, norm_out,
                     static_cast<cudaStream_t>(stream)));
   return SBP_OK;
 }
@@ -278,10 +289,8 @@ sbp_status sbp_grad_clip_norm(int64_t n, const float* const* grads, float* const
   if (!norm_out || !aligned(norm_out, 4))
     return fail(SBP_ERR_INVALID_ARG, "norm_out is NULL or misaligned");
   if (sbp_status s = check_ws(workspace, workspace_bytes, grad_norm_ws_bytes(n))) return s;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  double* sqsum = static_cast<double*>(workspace);      // the workspace's first 256 bytes
-  STEP_CK(grad_sqsum(n, grads, numel, sqsum, workspace, st));
-  STEP_CK(grad_clip(n, grads, outs, numel, sqsum, max_norm, norm_out, st));
+  STEP_CK(grad_clip_norm(tensors_of(n, grads, outs, numel), max_norm, norm_out, workspace,
+                         static_cast<cudaStream_t>(stream)));
   return SBP_OK;
 }
 

@@ -374,30 +374,30 @@ def embedding_backward(ids, dy2d, d_table, ws=None, stream=None):
 
 
 # ----------------------------------------------------------------------------- step operators
-def _device_of(stream, tensors):
-    """The one CUDA device of `tensors` (None entries are left out).  The library launches on
-    the current device, so the tensors and the stream have to be on it."""
+# These calls are short, so their checks are kept cheap: shapes are compared as they are (a
+# torch.Size is a tuple), pointers go to ctypes as integers.
+def _on_device(stream, *tensors):
+    """The index of the one CUDA device of `tensors` (None entries are left out) and the raw
+    stream.  The library launches on the current device: tensors and stream have to be its."""
     torch = _torch()
-    dev = None
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("tensors must be on a CUDA device")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on two devices, {dev} and {t.device}")
-    cur = torch.cuda.current_device()
-    if dev.index != cur or (stream is not None and stream.device != dev):
-        raise ValueError(f"tensors on {dev}: the current device and the stream must be its")
-    return dev
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors must be on one CUDA device")
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if dev != torch.cuda.current_device() or (stream is not None and stream.device.index != dev):
+        raise ValueError(f"tensors on cuda:{dev}: the current device and the stream must be its")
+    if stream is not None:
+        return dev, stream.cuda_stream
+    # the current stream's handle, without the Stream object that current_stream() makes (3 us)
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _is(t, name, dtype, shape):
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
@@ -406,30 +406,33 @@ def _is(t, name, dtype, shape):
 def _step_ws(ws, need, dev):
     if need == 0:
         raise SbpError(1, "invalid sizes")
-    if ws is None or ws.numel() * ws.element_size() < need:
-        return workspace(need, dev)
-    if not ws.is_contiguous() or ws.device != dev:
-        raise ValueError(f"the workspace must be a contiguous buffer on {dev}")
+    if ws is None or ws.nbytes < need:
+        return workspace(need, f"cuda:{dev}")
+    if not ws.is_contiguous() or ws.get_device() != dev:
+        raise ValueError(f"the workspace must be a contiguous buffer on cuda:{dev}")
     return ws
 
 
-def _nbytes(t):
-    return t.numel() * t.element_size()
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def embedding_scaled_forward(ids, table, scale, y, stream=None):
     """y[r] = scale * table[ids[r]]; ids int32, any shape; ids outside [0, vocab) give zero rows
     (include/sbp_step.h)."""
-    torch = _torch()
     V, cols = table.shape
     rows = ids.numel()
     dt = _dtype_code(table)
-    _is(ids, "ids", torch.int32, ids.shape)
-    _is(table, "table", table.dtype, (V, cols))
+    _is(ids, "ids", _torch().int32, ids.shape)
+    _is(table, "table", table.dtype, table.shape)
     _is(y, "y", table.dtype, (rows, cols) if y.dim() == 2 else (*ids.shape, cols))
-    _device_of(stream, (ids, table, y))
-    _check(load().sbp_embedding_scaled_forward(rows, cols, V, dt, scale, _ptr(ids), _ptr(table),
-                                               _ptr(y), _stream(stream)))
+    _, st = _on_device(stream, ids, table, y)
+    _check(load().sbp_embedding_scaled_forward(rows, cols, V, dt, scale, ids.data_ptr(),
+                                               table.data_ptr(), y.data_ptr(), st))
+
+
+def embedding_scaled_backward_workspace_size(rows, cols, vocab) -> int:
+    return int(load().sbp_embedding_scaled_backward_workspace_size(rows, cols, vocab))
 
 
 def embedding_scaled_backward(ids, dy, scale, d_table, accumulate=True, ws=None, stream=None):
@@ -439,14 +442,14 @@ def embedding_scaled_backward(ids, dy, scale, d_table, accumulate=True, ws=None,
     V, cols = d_table.shape
     rows = ids.numel()
     _is(ids, "ids", torch.int32, ids.shape)
-    _is(d_table, "d_table", torch.float32, (V, cols))
+    _is(d_table, "d_table", torch.float32, d_table.shape)
     _is(dy, "dy", torch.float32, (rows, cols) if dy.dim() == 2 else (*ids.shape, cols))
-    dev = _device_of(stream, (ids, dy, d_table))
-    lib = load()
-    ws = _step_ws(ws, lib.sbp_embedding_scaled_backward_workspace_size(rows, cols, V), dev)
-    _check(lib.sbp_embedding_scaled_backward(rows, cols, V, scale, _ptr(ids), _ptr(dy),
-                                             _ptr(d_table), int(accumulate), _ptr(ws),
-                                             _nbytes(ws), _stream(stream)))
+    dev, st = _on_device(stream, ids, dy, d_table)
+    ws = _step_ws(ws, embedding_scaled_backward_workspace_size(rows, cols, V), dev)
+    _check(load().sbp_embedding_scaled_backward(rows, cols, V, scale, ids.data_ptr(),
+                                                dy.data_ptr(), d_table.data_ptr(),
+                                                1 if accumulate else 0, ws.data_ptr(), ws.nbytes,
+                                                st))
     return ws
 
 
@@ -457,17 +460,17 @@ def rope_table(n_positions, head_dim, theta, device="cuda", stream=None):
         raise ValueError("rope_table: need positive sizes")
     cos = torch.empty(n_positions, head_dim // 2, dtype=torch.float32, device=device)
     sin = torch.empty_like(cos)
-    _device_of(stream, (cos,))
-    _check(load().sbp_rope_table(n_positions, head_dim, theta, _ptr(cos), _ptr(sin),
-                                 _stream(stream)))
+    _, st = _on_device(stream, cos)
+    _check(load().sbp_rope_table(n_positions, head_dim, theta, cos.data_ptr(), sin.data_ptr(),
+                                 st))
     return cos, sin
 
 
 def _heads(t, name, dtype, shape):
     """Row stride of a [rows, heads, head_dim] tensor whose rows may lie apart."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     rows, n, hd = shape
     sr, sh, s1 = t.stride()
@@ -480,26 +483,28 @@ def _heads(t, name, dtype, shape):
     return sr
 
 
-def _qk_call(q, k, q_g, k_g, cos, sin, eps, positions, seq_len, stream):
+def _qk_call(q, k, q_g, k_g, cos, sin, eps, positions, seq_len):
     """Checks of what both directions share; the configuration and the leading arguments."""
     torch = _torch()
+    dtype = q.dtype
     rows, H, hd = q.shape
-    Hkv = 0 if k is None else k.shape[1]
     dt = _dtype_code(q)
-    ldq = _heads(q, "q", q.dtype, (rows, H, hd))
-    _is(q_g, "q_g", q.dtype, (hd,))
-    ldk = 0
+    ldq = _heads(q, "q", dtype, q.shape)
+    _is(q_g, "q_g", dtype, (hd,))
+    Hkv = ldk = 0
     if k is not None:
-        ldk = _heads(k, "k", q.dtype, (rows, Hkv, hd))
-        _is(k_g, "k_g", q.dtype, (hd,))
-    table_len = cos.shape[0]
-    _is(cos, "cos", torch.float32, (table_len, hd // 2))
-    _is(sin, "sin", torch.float32, (table_len, hd // 2))
+        Hkv = k.shape[1]
+        ldk = _heads(k, "k", dtype, (rows, Hkv, hd))
+        _is(k_g, "k_g", dtype, (hd,))
+    table = (cos.shape[0], hd // 2)
+    _is(cos, "cos", torch.float32, table)
+    _is(sin, "sin", torch.float32, table)
     if positions is not None:
         _is(positions, "positions", torch.int32, (rows,))
-    cfg = QkCfg(rows, H, Hkv, hd, seq_len if seq_len is not None else rows, table_len, eps, dt)
-    return cfg, (C.byref(cfg), _ptr(q), ldq, _ptr(k), ldk, _ptr(q_g),
-                 _ptr(k_g) if k is not None else None, _ptr(positions), _ptr(cos), _ptr(sin))
+    cfg = QkCfg(rows, H, Hkv, hd, rows if seq_len is None else seq_len, table[0], eps, dt)
+    return cfg, (C.byref(cfg), q.data_ptr(), ldq, _addr(k), ldk, q_g.data_ptr(),
+                 None if k is None else k_g.data_ptr(), _addr(positions), cos.data_ptr(),
+                 sin.data_ptr())
 
 
 def qk_norm_rope_forward(q, k, q_g, k_g, cos, sin, eps, q_out, k_out, positions=None,
@@ -507,37 +512,38 @@ def qk_norm_rope_forward(q, k, q_g, k_g, cos, sin, eps, q_out, k_out, positions=
     """Per-head RMS norm with RoPE of q [rows, heads, head_dim] and k [rows, kv_heads, head_dim]
     (rows may be strided, k may be None) into q_out and k_out, which may be q and k
     (include/sbp_step.h).  The position of row r is positions[r], or r % seq_len (default: r)."""
-    cfg, args = _qk_call(q, k, q_g, k_g, cos, sin, eps, positions, seq_len, stream)
-    ldqo = _heads(q_out, "q_out", q.dtype, q.shape)
-    ldko = 0 if k is None else _heads(k_out, "k_out", q.dtype, k.shape)
-    _device_of(stream, (q, k, q_g, k_g, cos, sin, positions, q_out, k_out))
-    _check(load().sbp_qk_norm_rope_forward(*args, _ptr(q_out), ldqo,
-                                           _ptr(k_out) if k is not None else None, ldko,
-                                           _stream(stream)))
+    _, args = _qk_call(q, k, q_g, k_g, cos, sin, eps, positions, seq_len)
+    ldqo, ldko = _heads(q_out, "q_out", q.dtype, q.shape), 0
+    if k is None:
+        k_g = k_out = None
+    else:
+        ldko = _heads(k_out, "k_out", q.dtype, k.shape)
+    _, st = _on_device(stream, q, k, q_g, k_g, cos, sin, positions, q_out, k_out)
+    _check(load().sbp_qk_norm_rope_forward(*args, q_out.data_ptr(), ldqo, _addr(k_out), ldko, st))
 
 
 def qk_norm_rope_backward(q, k, q_g, k_g, cos, sin, eps, dq_out, dk_out, dq, dk, dq_g, dk_g,
                           positions=None, seq_len=None, ws=None, stream=None):
     """Backward of qk_norm_rope_forward from its inputs: dq, dk overwritten (they may be dq_out,
     dk_out), dq_g, dk_g accumulated; all gradients fp32.  Returns the workspace."""
-    torch = _torch()
-    f32 = torch.float32
-    cfg, args = _qk_call(q, k, q_g, k_g, cos, sin, eps, positions, seq_len, stream)
-    hd = q.shape[2]
-    ld = [_heads(dq_out, "dq_out", f32, q.shape), _heads(dq, "dq", f32, q.shape), 0, 0]
-    _is(dq_g, "dq_g", f32, (hd,))
+    f32 = _torch().float32
+    cfg, args = _qk_call(q, k, q_g, k_g, cos, sin, eps, positions, seq_len)
+    gain = (q.shape[2],)
+    lddqo, lddq = _heads(dq_out, "dq_out", f32, q.shape), _heads(dq, "dq", f32, q.shape)
+    _is(dq_g, "dq_g", f32, gain)
+    lddko = lddk = 0
     if k is None:
-        dk_out = dk = dk_g = None
+        k_g = dk_out = dk = dk_g = None
     else:
-        ld[2:] = [_heads(dk_out, "dk_out", f32, k.shape), _heads(dk, "dk", f32, k.shape)]
-        _is(dk_g, "dk_g", f32, (hd,))
-    dev = _device_of(stream, (q, k, q_g, k_g, cos, sin, positions, dq_out, dk_out, dq, dk, dq_g,
-                              dk_g))
+        lddko, lddk = _heads(dk_out, "dk_out", f32, k.shape), _heads(dk, "dk", f32, k.shape)
+        _is(dk_g, "dk_g", f32, gain)
+    dev, st = _on_device(stream, q, k, q_g, k_g, cos, sin, positions, dq_out, dk_out, dq, dk,
+                         dq_g, dk_g)
     lib = load()
-    ws = _step_ws(ws, lib.sbp_qk_norm_rope_backward_workspace_size(C.byref(cfg)), dev)
-    _check(lib.sbp_qk_norm_rope_backward(*args, _ptr(dq_out), ld[0], _ptr(dk_out), ld[2],
-                                         _ptr(dq), ld[1], _ptr(dk), ld[3], _ptr(dq_g),
-                                         _ptr(dk_g), _ptr(ws), _nbytes(ws), _stream(stream)))
+    ws = _step_ws(ws, lib.sbp_qk_norm_rope_backward_workspace_size(args[0]), dev)
+    _check(lib.sbp_qk_norm_rope_backward(*args, dq_out.data_ptr(), lddqo, _addr(dk_out), lddko,
+                                         dq.data_ptr(), lddq, _addr(dk), lddk, dq_g.data_ptr(),
+                                         _addr(dk_g), ws.data_ptr(), ws.nbytes, st))
     return ws
 
 
@@ -546,31 +552,34 @@ class GradList:
     pointers and sizes in host arrays.  It holds the tensors."""
 
     def __init__(self, tensors):
-        torch = _torch()
         self.tensors = list(tensors)
-        n = len(self.tensors)
+        if not self.tensors:
+            raise ValueError("no gradients")
+        f32, n = _torch().float32, len(self.tensors)
+        self.device = self.tensors[0].get_device()
         for i, t in enumerate(self.tensors):
-            _is(t, f"gradient {i}", torch.float32, t.shape)
-            if not t.is_cuda or t.device != self.tensors[0].device:
+            _is(t, f"gradient {i}", f32, t.shape)
+            if self.device < 0 or t.get_device() != self.device:
                 raise ValueError(f"gradient {i}: all gradients must be on one CUDA device")
+        self.sizes = [t.numel() for t in self.tensors]
         self.ptrs = (C.c_void_p * n)(*[t.data_ptr() for t in self.tensors])
-        self.numel = (C.c_int64 * n)(*[t.numel() for t in self.tensors])
+        self.numel = (C.c_int64 * n)(*self.sizes)
 
     def __len__(self):
         return len(self.tensors)
 
 
-def _grad_args(grads, out, scalars, stream):
-    grads = grads if isinstance(grads, GradList) else GradList(grads)
-    if len(grads) == 0:
-        raise ValueError("no gradients")
+def _grad_args(grads, out, stream, *scalars):
+    if not isinstance(grads, GradList):
+        grads = GradList(grads)
+    into = None
     if out is not None:
         out = out if isinstance(out, GradList) else GradList(out)
-        if len(out) != len(grads) or list(out.numel) != list(grads.numel):
-            raise ValueError("out must have the gradients' element counts")
-    dev = _device_of(stream, (grads.tensors[0], out.tensors[0] if out is not None else None,
-                              *scalars))
-    return grads, out, dev
+        if out.sizes != grads.sizes or out.device != grads.device:
+            raise ValueError("out must have the gradients' element counts and device")
+        into = out.ptrs
+    dev, st = _on_device(stream, grads.tensors[0], *scalars)
+    return grads, into, dev, st
 
 
 def grad_norm_workspace_size(n_tensors) -> int:
@@ -580,36 +589,33 @@ def grad_norm_workspace_size(n_tensors) -> int:
 def grad_sqsum(grads, sqsum, ws=None, stream=None):
     """sqsum[0] (float64) = the sum of the squares of all gradients (a GradList, or a list of
     fp32 tensors).  Returns the workspace."""
-    grads, _, dev = _grad_args(grads, None, (sqsum,), stream)
     _is(sqsum, "sqsum", _torch().float64, (1,))
+    grads, _, dev, st = _grad_args(grads, None, stream, sqsum)
     ws = _step_ws(ws, grad_norm_workspace_size(len(grads)), dev)
-    _check(load().sbp_grad_sqsum(len(grads), grads.ptrs, grads.numel, _ptr(sqsum), _ptr(ws),
-                                 _nbytes(ws), _stream(stream)))
+    _check(load().sbp_grad_sqsum(len(grads), grads.ptrs, grads.numel, sqsum.data_ptr(),
+                                 ws.data_ptr(), ws.nbytes, st))
     return ws
 
 
 def grad_clip(grads, sqsum, max_norm, norm_out=None, out=None, stream=None):
     """out (default: in place) = grads * min(1, max_norm / (sqrt(sqsum) + 1e-6))."""
     torch = _torch()
-    grads, out, _ = _grad_args(grads, out, (sqsum, norm_out), stream)
     _is(sqsum, "sqsum", torch.float64, (1,))
     if norm_out is not None:
         _is(norm_out, "norm_out", torch.float32, (1,))
-    _check(load().sbp_grad_clip(len(grads), grads.ptrs, out.ptrs if out is not None else None,
-                                grads.numel, _ptr(sqsum), max_norm, _ptr(norm_out),
-                                _stream(stream)))
+    grads, into, _, st = _grad_args(grads, out, stream, sqsum, norm_out)
+    _check(load().sbp_grad_clip(len(grads), grads.ptrs, into, grads.numel, sqsum.data_ptr(),
+                                max_norm, _addr(norm_out), st))
 
 
 def grad_clip_norm(grads, max_norm, norm_out, out=None, ws=None, stream=None):
     """norm_out[0] = the global norm of all gradients, which are clipped to max_norm (in place,
     or into `out`).  Returns the workspace."""
-    grads, out, dev = _grad_args(grads, out, (norm_out,), stream)
     _is(norm_out, "norm_out", _torch().float32, (1,))
+    grads, into, dev, st = _grad_args(grads, out, stream, norm_out)
     ws = _step_ws(ws, grad_norm_workspace_size(len(grads)), dev)
-    _check(load().sbp_grad_clip_norm(len(grads), grads.ptrs,
-                                     out.ptrs if out is not None else None, grads.numel,
-                                     max_norm, _ptr(norm_out), _ptr(ws), _nbytes(ws),
-                                     _stream(stream)))
+    _check(load().sbp_grad_clip_norm(len(grads), grads.ptrs, into, grads.numel, max_norm,
+                                     norm_out.data_ptr(), ws.data_ptr(), ws.nbytes, st))
     return ws
 
 

@@ -45,6 +45,8 @@ EMBED = [  # rows, cols, vocab, kind of ids
     (5000, 36, 130000, "two"), (8191, 4, 128256, "zipf"), (8193, 20, 152064, "zipf"),
     (20011, 132, 700, "padded"), (70001, 8, 200000, "zipf"), (40000, 3, 4096, "same"),
     (66000, 2, 1 << 22, "ends"), (17000, 24, 300, "sorted"), (16385, 24, 300, "reversed"),
+    (256, 36, 1, "same"), (255, 130, 128256, "two"), (256, 4100, 30, "ends"), (257, 8, 4, "zipf"),
+    (4096, 8, 5000, "zipf"), (4097, 8, 5000, "padded"), (300, 2, 200000, "uniform"),
 ]
 
 
@@ -339,7 +341,10 @@ def grad_list(sizes, g, scale=1.0, spread=2.0):
 SIZES = {
     "one": [1], "odd": [1, 2, 3, 4, 5, 0, 7, 1023, 16383, 16384, 16385, 0, 65537],
     "empty": [0, 0], "many": [(i * 37) % 1201 for i in range(700)], "large": [3_000_001, 17],
-    "exactly_full": [5] * 256, "one_more": [5] * 257,
+    "few": [131072], "above_few": [131073], "full_table": [5] * 64, "one_more": [5] * 65,
+    "full_large_table": [130] * 1024, "one_more_large": [130] * 1025,
+    "small_among_large": [1] * 900 + [2_000_001] + [3] * 200 + [4_000_000],
+    "thousands": [3] * 2500, "pieces": [4 * 1024 * k + k % 3 for k in range(1, 70)],
 }
 
 
