@@ -90,6 +90,33 @@ sbp_status sbp_qk_norm_rope_backward(const sbp_qk_cfg* cfg, const void* q, int64
                                      float* dk, int64_t lddk, float* dq_g, float* dk_g,
                                      void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * The decoder layer of sbp.h with these norms between its projections and the attention (eps =
+ * cfg->rms_eps; biases, where given, come before the norm):
+ *   q = rope(norm(n1 W_q^T + b_q; q_g)),  k = rope(norm(n1 W_k^T + b_k; k_g))   per head
+ * Arguments, layouts, accumulation and errors are those of sbp_decoder_layer_forward_stream and
+ * sbp_decoder_layer_backward_stream (or, with `reverse`, its _reverse form).  The projections
+ * are rounded to cfg->dtype before the norm; only one chunk of them is kept, the backward forms
+ * the keys' again.  dq_g, dk_g: device fp32 [head_dim], accumulated.
+ */
+typedef struct { /* device [head_dim], cfg.dtype, 16-byte aligned */
+  const void *q_g, *k_g;
+} sbp_qk_gains;
+
+size_t sbp_decoder_layer_qk_norm_workspace_size(const sbp_layer_cfg* cfg);
+sbp_status sbp_decoder_layer_qk_norm_forward_stream(const sbp_layer_cfg* cfg,
+                                                    const sbp_layer_weights* w,
+                                                    const sbp_qk_gains* gains, const void* x,
+                                                    void* y, void* workspace,
+                                                    size_t workspace_bytes, void* stream);
+sbp_status sbp_decoder_layer_qk_norm_backward_stream(const sbp_layer_cfg* cfg,
+                                                     const sbp_layer_weights* w,
+                                                     const sbp_qk_gains* gains, const void* x,
+                                                     const float* dy, float* dx,
+                                                     const sbp_layer_grads* grads, float* dq_g,
+                                                     float* dk_g, int reverse, void* workspace,
+                                                     size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------------------------------------
  * Global gradient norm over many tensors, and clipping:
  *   norm = sqrt(sum over all tensors and elements of g^2)          (products and sums in 64 bits)

@@ -15,6 +15,7 @@
 #include "sbp_debug.h"
 #include "sbp_dpo.h"
 #include "sbp_internal.cuh"
+#include "sbp_step.h"
 
 using namespace sbp;
 
@@ -113,6 +114,10 @@ struct LayerPlan {
   float *dyg, *rstd1, *qkv, *alse, *hbuf, *rstd2, *dn2, *dh, *delta, *dq, *dn1, *dxg;
   float *dkpre, *dvg, *rpart, *cpart;
   int* aflags;   // the attention forward's split flags (its partials use dq and delta)
+  // with query/key norms: the chunk's projections before the norm, the values before they go to
+  // the prefix, the blocks' partial gain gradients
+  void *qraw, *kraw, *vraw;
+  float* gpart;
   // bf16 operand copies of fp32 gradients (bf16 path only)
   void *dyg16, *dh16, *dq16, *khi, *klo, *vhi, *vlo;
   int64_t R;
@@ -125,7 +130,7 @@ bool qkv_fused(const sbp_layer_cfg& L) {
   return L.dtype == SBP_BF16 && L.head_dim == 128 && L.d_model % 8 == 0;
 }
 
-void layer_carve(Carver& c, const sbp_layer_cfg& L, LayerPlan& p) {
+void layer_carve(Carver& c, const sbp_layer_cfg& L, LayerPlan& p, bool qk_norm = false) {
   const int dt = L.dtype;
   const size_t es = dt_size(dt);
   const int64_t B = L.batch, T = L.seq_len, d = L.d_model, f = L.ffn;
@@ -144,7 +149,7 @@ void layer_carve(Carver& c, const sbp_layer_cfg& L, LayerPlan& p) {
   p.n1 = c.take_bytes((size_t)R * d * es);
   p.rstd1 = c.take<float>(R);
   // fp32 staging of the Q/K/V projections: only where RoPE is not done in the GEMM epilogue
-  p.qkv = c.take<float>(qkv_fused(L) ? 0 : (size_t)R * (dq + 2 * dkv));
+  p.qkv = c.take<float>(qkv_fused(L) || qk_norm ? 0 : (size_t)R * (dq + 2 * dkv));
   p.q = c.take_bytes((size_t)R * dq * es);
   p.o = c.take_bytes((size_t)R * dq * es);
   p.alse = c.take<float>((size_t)R * L.n_heads);
@@ -177,6 +182,16 @@ void layer_carve(Carver& c, const sbp_layer_cfg& L, LayerPlan& p) {
     p.vhi = c.take_bytes((size_t)R * dkv * 2);
     p.vlo = c.take_bytes((size_t)R * dkv * 2);
   }
+  p.qraw = p.kraw = p.vraw = nullptr;
+  p.gpart = nullptr;
+  if (qk_norm) {
+    p.qraw = c.take_bytes((size_t)R * dq * es);
+    p.kraw = c.take_bytes((size_t)R * dkv * es);
+    p.vraw = c.take_bytes((size_t)R * dkv * es);
+    const size_t nq = qk_norm_bwd_partial_floats(R, L.n_heads, 0, L.head_dim);
+    const size_t nk = qk_norm_bwd_partial_floats(R, L.n_kv_heads, 0, L.head_dim);
+    p.gpart = c.take<float>(nq > nk ? nq : nk);
+  }
 }
 
 // GEMM descriptor helpers.  Matrices are row-major with the given leading dimension.
@@ -202,6 +217,12 @@ GemmDesc over_tokens(GemmDesc g) {
   g.kblk = kTokenBlock;
   return g;
 }
+
+// The gains of the query/key norms and their gradients (null in a forward).
+struct QkGains {
+  const void *q_g, *k_g;
+  float *dq_g, *dk_g;
+};
 
 sbp_status check_layer_cfg(const sbp_layer_cfg* L) {
   if (!L) return fail(SBP_ERR_INVALID_ARG, "cfg is NULL");
@@ -268,16 +289,83 @@ sbp_status qkv_project(const sbp_layer_cfg& L, const sbp_layer_weights& w, const
   return SBP_OK;
 }
 
+// One tensor's norm with RoPE for a chunk: heads of p.qraw or p.kraw, positions s ...
+QkNorm qk_norm_of(const sbp_layer_cfg& L, const LayerPlan& p, int64_t s, int64_t Tc) {
+  QkNorm a;
+  a.rows = L.batch * Tc;
+  a.hd = L.head_dim;
+  a.dt = L.dtype;
+  a.eps = L.rms_eps;
+  a.seq_len = Tc;
+  a.pos0 = s;
+  a.table_len = L.seq_len;
+  a.cosb = p.cosb;
+  a.sinb = p.sinb;
+  return a;
+}
+
+// The key projection of a chunk before its norm: kraw = n1 W_k^T (+ b_k).
+sbp_status k_project_raw(const sbp_layer_cfg& L, const sbp_layer_weights& w, const LayerPlan& p,
+                         int64_t Tc, cudaStream_t st) {
+  const int64_t d = L.d_model, dkv = L.n_kv_heads * L.head_dim;
+  GemmDesc g = mk_gemm(L.batch * Tc, dkv, d, L.dtype, p.n1, false, d, L.dtype, w.wk, true, d,
+                       L.dtype, p.kraw, dkv, EPI_STORE);
+  g.bias = w.bk; g.bias_dt = L.dtype;
+  SBP_CK(gemm(g, st));
+  return SBP_OK;
+}
+
+// Q / K / V projections of a chunk with query/key norms: q and the K prefix rows are normed and
+// rotated in one pass over the projections (rounded to the operand dtype before the norm, as the
+// backward reads them again), V goes to its prefix rows.
+sbp_status qkv_project_normed(const sbp_layer_cfg& L, const sbp_layer_weights& w,
+                              const QkGains& qk, const LayerPlan& p, int64_t s, int64_t Tc,
+                              int part, cudaStream_t st) {
+  const int dt = L.dtype;
+  const int64_t B = L.batch, T = L.seq_len, d = L.d_model, R = B * Tc;
+  const int64_t dq = L.n_heads * L.head_dim, dkv = L.n_kv_heads * L.head_dim;
+  QkNorm a = qk_norm_of(L, p, s, Tc);
+  if (part != QKV_KV) {
+    GemmDesc g = mk_gemm(R, dq, d, dt, p.n1, false, d, dt, w.wq, true, d, dt, p.qraw, dq,
+                         EPI_STORE);
+    g.bias = w.bq; g.bias_dt = dt;
+    SBP_CK(gemm(g, st));
+    a.q.n = L.n_heads;
+    a.q.x = p.qraw;
+    a.q.g = qk.q_g;
+    a.q.y = p.q;
+    a.q.ldx = a.q.ldy = dq;
+  }
+  if (part != QKV_Q) {
+    if (sbp_status r = k_project_raw(L, w, p, Tc, st)) return r;
+    a.k.n = L.n_kv_heads;
+    a.k.x = p.kraw;
+    a.k.g = qk.k_g;
+    a.k.y = p.Kp;
+    a.k.ldx = a.k.ldy = dkv;
+    a.k_T = T;
+    GemmDesc g = mk_gemm(R, dkv, d, dt, p.n1, false, d, dt, w.wv, true, d, dt, p.vraw, dkv,
+                         EPI_STORE);
+    g.bias = w.bv; g.bias_dt = dt;
+    SBP_CK(gemm(g, st));
+    SBP_CK(scatter_chunk(B, T, Tc, s, dkv, dt, p.vraw, p.Vp, st));
+  }
+  SBP_CK(qk_norm_rope_fwd(a, st));
+  return SBP_OK;
+}
+
 // RMSNorm-1 and the K/V projections of one chunk: fills n1, rstd1 and the chunk's rows of the
 // K/V prefix.  xc is the chunk's input rows [B * Tc, d] (contiguous).
-sbp_status layer_chunk_kv(const sbp_layer_cfg& L, const sbp_layer_weights& w, const LayerPlan& p,
-                          const void* xc, int64_t s, int64_t Tc, cudaStream_t st) {
+sbp_status layer_chunk_kv(const sbp_layer_cfg& L, const sbp_layer_weights& w, const QkGains* qk,
+                          const LayerPlan& p, const void* xc, int64_t s, int64_t Tc,
+                          cudaStream_t st) {
   const int dt = L.dtype;
   const int64_t B = L.batch, T = L.seq_len, d = L.d_model;
   const int64_t H = L.n_heads, Hkv = L.n_kv_heads, hd = L.head_dim;
   const int64_t dq = H * hd, dkv = Hkv * hd, W3 = dq + 2 * dkv;
   const int64_t R = B * Tc;
   SBP_CK(rmsnorm_fwd(R, d, dt, xc, dt, w.ln1_g, dt, p.n1, p.rstd1, L.rms_eps, st));
+  if (qk) return qkv_project_normed(L, w, *qk, p, s, Tc, QKV_KV, st);
   if (qkv_fused(L)) return qkv_project(L, w, p, s, Tc, QKV_KV, st);
   GemmDesc g = mk_gemm(R, dkv, d, dt, p.n1, false, d, dt, w.wk, true, d, DT_F32, p.qkv + dq, W3,
                        EPI_STORE);
@@ -296,15 +384,19 @@ sbp_status layer_chunk_kv(const sbp_layer_cfg& L, const sbp_layer_weights& w, co
 // n2, rstd2, gu and m.  xc is the chunk's input rows [B * Tc, d] (contiguous).  With
 // kv_ready the whole K/V prefix is already in place: only the query projection is computed.
 sbp_status layer_chunk_forward(const sbp_layer_cfg& L, const sbp_layer_weights& w,
-                               const LayerPlan& p, const void* xc, int64_t s, int64_t Tc,
-                               cudaStream_t st, bool kv_ready = false) {
+                               const QkGains* qk, const LayerPlan& p, const void* xc, int64_t s,
+                               int64_t Tc, cudaStream_t st, bool kv_ready = false) {
   const int dt = L.dtype;
   const int64_t B = L.batch, T = L.seq_len, d = L.d_model, f = L.ffn;
   const int64_t H = L.n_heads, Hkv = L.n_kv_heads, hd = L.head_dim;
   const int64_t dq = H * hd, dkv = Hkv * hd, W3 = dq + 2 * dkv;
   const int64_t R = B * Tc;
   SBP_CK(rmsnorm_fwd(R, d, dt, xc, dt, w.ln1_g, dt, p.n1, p.rstd1, L.rms_eps, st));
-  if (qkv_fused(L)) {
+  if (qk) {
+    const sbp_status r =
+        qkv_project_normed(L, w, *qk, p, s, Tc, kv_ready ? QKV_Q : QKV_ALL, st);
+    if (r != SBP_OK) return r;
+  } else if (qkv_fused(L)) {
     const sbp_status r = qkv_project(L, w, p, s, Tc, kv_ready ? QKV_Q : QKV_ALL, st);
     if (r != SBP_OK) return r;
   } else {
@@ -715,7 +807,7 @@ size_t sbp_decoder_layer_workspace_size(const sbp_layer_cfg* cfg) {
 // first; when chunk i is reached every chunk that attends to its keys is done, so its K/V
 // projection backward runs inside the same iteration, on the n1 rows already in place.
 static sbp_status layer_backward_run(const sbp_layer_cfg* cfg, const sbp_layer_weights* w,
-                                     const void* x, const float* dy, float* dx,
+                                     const QkGains* qk, const void* x, const float* dy, float* dx,
                                      const sbp_layer_grads* gr, void* workspace,
                                      size_t workspace_bytes, void* stream, bool reverse) {
   if (sbp_status s = check_layer_cfg(cfg)) return s;
@@ -735,13 +827,14 @@ static sbp_status layer_backward_run(const sbp_layer_cfg* cfg, const sbp_layer_w
   for (const void* q : io)
     if (!q || !aligned16(q)) return fail(SBP_ERR_INVALID_ARG, "x/dy/dx NULL or misaligned");
   const sbp_layer_cfg& L = *cfg;
-  const size_t need = sbp_decoder_layer_workspace_size(cfg);
+  const size_t need = qk ? sbp_decoder_layer_qk_norm_workspace_size(cfg)
+                         : sbp_decoder_layer_workspace_size(cfg);
   if (sbp_status s = check_ws(workspace, workspace_bytes, need)) return s;
 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Carver c(workspace);
   LayerPlan p;
-  layer_carve(c, L, p);
+  layer_carve(c, L, p, qk != nullptr);
   const int dt = L.dtype;
   const size_t es = dt_size(dt);
   const int64_t B = L.batch, T = L.seq_len, d = L.d_model, f = L.ffn;
@@ -786,12 +879,24 @@ static sbp_status layer_backward_run(const sbp_layer_cfg* cfg, const sbp_layer_w
     const int64_t R = B * Tc;
     // without biases the fp32 chunk rows of dK / dV are not needed: the bf16 path reads the
     // prefix rows, rotates dK and writes the hi + lo operands in one pass each
-    const bool fused = dt == DT_BF16 && !has_bias &&
+    const bool fused = dt == DT_BF16 && !has_bias && !qk &&
                        gather_split_ok(hd, dkv, p.dKp, p.khi, p.klo, p.cosb, p.sinb) &&
                        gather_split_ok(hd, dkv, p.dVp, p.vhi, p.vlo, p.cosb, p.sinb);
     if (fused) {
       SBP_CK(gather_rope_inv_split(B, T, Tc, s, Hkv, hd, p.dKp, p.khi, p.klo, p.cosb, p.sinb, st));
       SBP_CK(gather_split_bf16(B, T, Tc, s, dkv, p.dVp, p.vhi, p.vlo, st));
+    } else if (qk) {
+      // the projection before its norm is formed again from n1: only one chunk of it is kept
+      if (sbp_status r = k_project_raw(L, *w, p, Tc, st)) return r;
+      SBP_CK(gather_chunk(B, T, Tc, s, dkv, DT_F32, p.dKp, p.dkpre, st));
+      QkNorm a = qk_norm_of(L, p, s, Tc);
+      a.q.n = Hkv;
+      a.q.x = p.kraw;
+      a.q.g = qk->k_g;
+      a.q.dy = a.q.dx = p.dkpre;
+      a.q.ldx = a.q.lddy = a.q.lddx = dkv;
+      SBP_CK(qk_norm_rope_bwd(a, qk->dk_g, nullptr, p.gpart, st));
+      SBP_CK(gather_chunk(B, T, Tc, s, dkv, DT_F32, p.dVp, p.dvg, st));
     } else {
       SBP_CK(gather_rope_inv(B, T, Tc, s, Hkv, hd, p.dKp, p.dkpre, p.cosb, p.sinb, st));
       SBP_CK(gather_chunk(B, T, Tc, s, dkv, DT_F32, p.dVp, p.dvg, st));
@@ -841,7 +946,7 @@ static sbp_status layer_backward_run(const sbp_layer_cfg* cfg, const sbp_layer_w
         SBP_CK(gather_chunk(B, T, Tc, s, d, dt, x, p.xg, st));
         xc = p.xg;
       }
-      if (sbp_status r = layer_chunk_kv(L, *w, p, xc, s, Tc, st)) return r;
+      if (sbp_status r = layer_chunk_kv(L, *w, qk, p, xc, s, Tc, st)) return r;
     }
   }
 
@@ -861,7 +966,7 @@ static sbp_status layer_backward_run(const sbp_layer_cfg* cfg, const sbp_layer_w
       dyc = p.dyg;
       dxc = p.dxg;
     }
-    if (sbp_status r = layer_chunk_forward(L, *w, p, xc, s, Tc, st, reverse)) return r;
+    if (sbp_status r = layer_chunk_forward(L, *w, qk, p, xc, s, Tc, st, reverse)) return r;
     // ---- MLP backward.  fp32 gradients enter the tensor cores as bf16 operands (rounded
     // per element, so the rounding does not depend on the chunking).
     const bool b16 = dt == DT_BF16;
@@ -913,7 +1018,17 @@ static sbp_status layer_backward_run(const sbp_layer_cfg* cfg, const sbp_layer_w
     // ---- attention backward over the causal prefix; dK/dV accumulate in fp32
     SBP_CK(attn_bwd(B, T, Tc, s, H, Hkv, hd, dt, p.q, p.Kp, p.Vp, p.o, p.dO, p.alse, p.delta,
                     p.dq, p.dKp, p.dVp, st));
-    SBP_CK(rope_inv_f32(R, Tc, s, H, hd, p.dq, p.cosb, p.sinb, st));
+    if (qk) {
+      QkNorm a = qk_norm_of(L, p, s, Tc);
+      a.q.n = H;
+      a.q.x = p.qraw;
+      a.q.g = qk->q_g;
+      a.q.dy = a.q.dx = p.dq;
+      a.q.ldx = a.q.lddy = a.q.lddx = dq;
+      SBP_CK(qk_norm_rope_bwd(a, qk->dq_g, nullptr, p.gpart, st));
+    } else {
+      SBP_CK(rope_inv_f32(R, Tc, s, H, hd, p.dq, p.cosb, p.sinb, st));
+    }
     // ---- q projection backward
     // dQ of a query row is a fixed-order sum over its key tiles (the same at every D), so a
     // plain per-element bf16 rounding is D-independent
@@ -969,7 +1084,8 @@ sbp_status sbp_decoder_layer_backward_stream(const sbp_layer_cfg* cfg,
                                              const float* dy, float* dx,
                                              const sbp_layer_grads* gr, void* workspace,
                                              size_t workspace_bytes, void* stream) {
-  return layer_backward_run(cfg, w, x, dy, dx, gr, workspace, workspace_bytes, stream, false);
+  return layer_backward_run(cfg, w, nullptr, x, dy, dx, gr, workspace, workspace_bytes, stream,
+                            false);
 }
 
 sbp_status sbp_decoder_layer_backward_stream_reverse(const sbp_layer_cfg* cfg,
@@ -978,25 +1094,26 @@ sbp_status sbp_decoder_layer_backward_stream_reverse(const sbp_layer_cfg* cfg,
                                                      const sbp_layer_grads* gr,
                                                      void* workspace, size_t workspace_bytes,
                                                      void* stream) {
-  return layer_backward_run(cfg, w, x, dy, dx, gr, workspace, workspace_bytes, stream, true);
+  return layer_backward_run(cfg, w, nullptr, x, dy, dx, gr, workspace, workspace_bytes, stream,
+                            true);
 }
 
-sbp_status sbp_decoder_layer_forward_stream(const sbp_layer_cfg* cfg,
-                                            const sbp_layer_weights* w, const void* x, void* y,
-                                            void* workspace, size_t workspace_bytes,
-                                            void* stream) {
+static sbp_status layer_forward_run(const sbp_layer_cfg* cfg, const sbp_layer_weights* w,
+                                    const QkGains* qk, const void* x, void* y, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
   if (sbp_status s = check_layer_cfg(cfg)) return s;
   bool has_bias = false;
   if (sbp_status s = check_weights(w, &has_bias)) return s;
   if (!x || !y || !aligned16(x) || !aligned16(y))
     return fail(SBP_ERR_INVALID_ARG, "x/y NULL or misaligned");
   const sbp_layer_cfg& L = *cfg;
-  const size_t need = sbp_decoder_layer_workspace_size(cfg);
+  const size_t need = qk ? sbp_decoder_layer_qk_norm_workspace_size(cfg)
+                         : sbp_decoder_layer_workspace_size(cfg);
   if (sbp_status s = check_ws(workspace, workspace_bytes, need)) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Carver c(workspace);
   LayerPlan p;
-  layer_carve(c, L, p);
+  layer_carve(c, L, p, qk != nullptr);
   const int dt = L.dtype;
   const int64_t B = L.batch, T = L.seq_len, d = L.d_model, f = L.ffn;
   tl_status = p.status;
@@ -1016,7 +1133,7 @@ sbp_status sbp_decoder_layer_forward_stream(const sbp_layer_cfg* cfg,
       SBP_CK(gather_chunk(B, T, Tc, s, d, dt, x, p.xg, st));
       xc = p.xg;
     }
-    if (sbp_status r = layer_chunk_forward(L, *w, p, xc, s, Tc, st)) return r;
+    if (sbp_status r = layer_chunk_forward(L, *w, qk, p, xc, s, Tc, st)) return r;
     SBP_CK(gemm(mk_gemm(R, d, f, dt, p.m, false, f, dt, w->w_down, true, f, DT_F32, p.hbuf, d,
                         EPI_ACC), st));
     if (B > 1) {
@@ -1028,6 +1145,54 @@ sbp_status sbp_decoder_layer_forward_stream(const sbp_layer_cfg* cfg,
     }
   }
   return SBP_OK;
+}
+
+sbp_status sbp_decoder_layer_forward_stream(const sbp_layer_cfg* cfg,
+                                            const sbp_layer_weights* w, const void* x, void* y,
+                                            void* workspace, size_t workspace_bytes,
+                                            void* stream) {
+  return layer_forward_run(cfg, w, nullptr, x, y, workspace, workspace_bytes, stream);
+}
+
+// The layer with query/key norms (sbp_step.h).
+static sbp_status check_qk_gains(const sbp_qk_gains* g) {
+  if (!g) return fail(SBP_ERR_INVALID_ARG, "the gains are NULL");
+  if (!g->q_g || !g->k_g || !aligned16(g->q_g) || !aligned16(g->k_g))
+    return fail(SBP_ERR_INVALID_ARG, "a gain is NULL or not 16-byte aligned");
+  return SBP_OK;
+}
+
+size_t sbp_decoder_layer_qk_norm_workspace_size(const sbp_layer_cfg* cfg) {
+  if (check_layer_cfg(cfg) != SBP_OK) return 0;
+  Carver c(nullptr);
+  LayerPlan p;
+  layer_carve(c, *cfg, p, true);
+  return c.off;
+}
+
+sbp_status sbp_decoder_layer_qk_norm_forward_stream(const sbp_layer_cfg* cfg,
+                                                    const sbp_layer_weights* w,
+                                                    const sbp_qk_gains* gains, const void* x,
+                                                    void* y, void* workspace,
+                                                    size_t workspace_bytes, void* stream) {
+  if (sbp_status s = check_qk_gains(gains)) return s;
+  const QkGains qk = {gains->q_g, gains->k_g, nullptr, nullptr};
+  return layer_forward_run(cfg, w, &qk, x, y, workspace, workspace_bytes, stream);
+}
+
+sbp_status sbp_decoder_layer_qk_norm_backward_stream(const sbp_layer_cfg* cfg,
+                                                     const sbp_layer_weights* w,
+                                                     const sbp_qk_gains* gains, const void* x,
+                                                     const float* dy, float* dx,
+                                                     const sbp_layer_grads* grads, float* dq_g,
+                                                     float* dk_g, int reverse, void* workspace,
+                                                     size_t workspace_bytes, void* stream) {
+  if (sbp_status s = check_qk_gains(gains)) return s;
+  if (!dq_g || !dk_g || !aligned16(dq_g) || !aligned16(dk_g))
+    return fail(SBP_ERR_INVALID_ARG, "a gain gradient is NULL or not 16-byte aligned");
+  const QkGains qk = {gains->q_g, gains->k_g, dq_g, dk_g};
+  return layer_backward_run(cfg, w, &qk, x, dy, dx, grads, workspace, workspace_bytes, stream,
+                            reverse != 0);
 }
 
 // ------------------------------------------------------------------------------- support

@@ -46,7 +46,8 @@ def stack_buckets(layers: List[dict], lm_shape, final_shape, embed_shape) -> Lis
     plan = [("head", [("lm_head", tuple(lm_shape)), ("final_g", tuple(final_shape))])]
     for li in range(len(layers) - 1, -1, -1):
         W = layers[li]
-        plan.append((f"layer{li}", [(n, tuple(W[n].shape)) for n in sbp.WEIGHT_FIELDS
+        plan.append((f"layer{li}", [(n, tuple(W[n].shape))
+                                    for n in sbp.WEIGHT_FIELDS + sbp.QK_NORM_FIELDS
                                     if W.get(n) is not None]))
     plan.append(("embed", [("embed", tuple(embed_shape))]))
     return plan
@@ -94,7 +95,8 @@ class ShardedGrads:
              "embed": self.views["embed"]["embed"], "layers": []}
         for li in range(n_layers):
             v = self.views[f"layer{li}"]
-            g["layers"].append({n: v.get(n) for n in sbp.WEIGHT_FIELDS})
+            names = sbp.WEIGHT_FIELDS + tuple(n for n in sbp.QK_NORM_FIELDS if n in v)
+            g["layers"].append({n: v.get(n) for n in names})
         return g
 
 
@@ -135,8 +137,27 @@ class GradReducer:
         self.issued.clear()
 
 
+def clip_sharded(grads: ShardedGrads, max_norm: float, group=None, ws=None):
+    """Clips this rank's reduced shards in place to the global norm `max_norm` of the whole
+    gradient: the ranks add their sums of squares (one fp64 scalar is exchanged).  Returns the
+    norm before the clipping (device fp32 [1], the same on every rank).  Every rank calls it,
+    after `GradReducer.wait`."""
+    import torch
+    import torch.distributed as dist
+    shards = sbp.GradList([grads.out[b] for b in grads.order])
+    dev = shards.tensors[0].device
+    sqsum = torch.empty(1, dtype=torch.float64, device=dev)
+    norm = torch.empty(1, dtype=torch.float32, device=dev)
+    sbp.grad_sqsum(shards, sqsum, ws=ws)
+    if group is not None or dist.is_initialized():
+        dist.all_reduce(sqsum, op=dist.ReduceOp.SUM, group=group)
+    sbp.grad_clip(shards, sqsum, max_norm, norm_out=norm)
+    return norm
+
+
 def dp_stack_step(cfg: sbp.LayerCfg, embed, layers: List[dict], final_g, lm_w, ids, targets,
-                  loss_weights, grads: ShardedGrads, reducer: GradReducer, ws=None):
+                  loss_weights, grads: ShardedGrads, reducer: GradReducer, ws=None,
+                  embed_scale=None):
     """One data-parallel step on this rank's sequences: forward (layer-input checkpoints),
     streamed backward with the bucket reduce-scatters queued as each bucket is final, wait.
     Runs on torch's current stream (the collectives are ordered after it).  The loss weights
@@ -145,9 +166,10 @@ def dp_stack_step(cfg: sbp.LayerCfg, embed, layers: List[dict], final_g, lm_w, i
     from . import stack
     ws = ws or stack.Workspaces(embed.device)
     grads.zero_()
-    xs, hf, rstd = stack.stack_forward(cfg, embed, layers, final_g, ids, ws)
+    xs, hf, rstd = stack.stack_forward(cfg, embed, layers, final_g, ids, ws,
+                                       embed_scale=embed_scale)
     res = stack.stack_backward_from(cfg, layers, final_g, lm_w, ids, targets, loss_weights, xs,
                                     hf, rstd, ws, grads=grads.stack_grads(len(layers)),
-                                    on_final=reducer.ready)
+                                    on_final=reducer.ready, embed_scale=embed_scale)
     reducer.wait()
     return res.loss

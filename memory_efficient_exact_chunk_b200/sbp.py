@@ -33,11 +33,14 @@ EXPORTS = [
     "sbp_embedding_scaled_backward_workspace_size", "sbp_embedding_scaled_backward",
     "sbp_rope_table", "sbp_qk_norm_rope_forward", "sbp_qk_norm_rope_backward_workspace_size",
     "sbp_qk_norm_rope_backward", "sbp_grad_norm_workspace_size", "sbp_grad_sqsum",
-    "sbp_grad_clip", "sbp_grad_clip_norm",
+    "sbp_grad_clip", "sbp_grad_clip_norm", "sbp_decoder_layer_qk_norm_workspace_size",
+    "sbp_decoder_layer_qk_norm_forward_stream", "sbp_decoder_layer_qk_norm_backward_stream",
 ]
 
 WEIGHT_FIELDS = ("ln1_g", "wq", "wk", "wv", "bq", "bk", "bv", "wo", "ln2_g", "w_gate", "w_up",
                  "w_down")
+# gains of the per-head norms of queries and keys, which a layer may have besides (sbp_step.h)
+QK_NORM_FIELDS = ("q_norm_g", "k_norm_g")
 
 
 class SbpError(RuntimeError):
@@ -64,6 +67,10 @@ class LayerWeights(C.Structure):
 
 class LayerGrads(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in WEIGHT_FIELDS]
+
+
+class QkGains(C.Structure):
+    _fields_ = [("q_g", C.c_void_p), ("k_g", C.c_void_p)]
 
 
 class QkCfg(C.Structure):
@@ -133,6 +140,13 @@ def load(path: Optional[str] = None):
     lib.sbp_qk_norm_rope_backward_workspace_size.argtypes = [C.POINTER(QkCfg)]
     lib.sbp_qk_norm_rope_backward.argtypes = [C.POINTER(QkCfg), vp, i64, vp, i64] + [vp] * 5 + \
         [vp, i64] * 4 + [vp, vp, vp, sz, vp]
+    lib.sbp_decoder_layer_qk_norm_workspace_size.restype = sz
+    lib.sbp_decoder_layer_qk_norm_workspace_size.argtypes = [C.POINTER(LayerCfg)]
+    lib.sbp_decoder_layer_qk_norm_forward_stream.argtypes = [
+        C.POINTER(LayerCfg), C.POINTER(LayerWeights), C.POINTER(QkGains), vp, vp, vp, sz, vp]
+    lib.sbp_decoder_layer_qk_norm_backward_stream.argtypes = [
+        C.POINTER(LayerCfg), C.POINTER(LayerWeights), C.POINTER(QkGains), vp, vp, vp,
+        C.POINTER(LayerGrads), vp, vp, C.c_int, vp, sz, vp]
     lib.sbp_grad_norm_workspace_size.restype = sz
     lib.sbp_grad_norm_workspace_size.argtypes = [i64]
     lib.sbp_grad_sqsum.argtypes = [i64, vp, vp, vp, vp, sz, vp]
@@ -296,44 +310,88 @@ def _struct(cls, tensors: Dict[str, object]):
                   for n in WEIGHT_FIELDS})
 
 
-def layer_workspace_size(cfg: LayerCfg) -> int:
-    return load().sbp_decoder_layer_workspace_size(C.byref(cfg))
+def has_qk_norm(weights) -> bool:
+    """Whether a layer's weights name the gains of query/key norms (both or none)."""
+    n = sum(weights.get(f) is not None for f in QK_NORM_FIELDS)
+    if n == 1:
+        raise ValueError("q_norm_g and k_norm_g must be both set or both absent")
+    return n == 2
 
 
-def _layer_backward(fn, cfg, weights, x, dy, dx, grads, ws, stream):
-    need = layer_workspace_size(cfg)
+def layer_workspace_size(cfg: LayerCfg, qk_norm: bool = False) -> int:
+    lib = load()
+    if qk_norm:
+        return lib.sbp_decoder_layer_qk_norm_workspace_size(C.byref(cfg))
+    return lib.sbp_decoder_layer_workspace_size(C.byref(cfg))
+
+
+def _layer_ws(cfg, qk_norm, ws, device):
+    need = layer_workspace_size(cfg, qk_norm)
     if need == 0:
         raise SbpError(1, "invalid layer configuration")
-    if ws is None:
-        ws = workspace(need, x.device)
+    return workspace(need, device) if ws is None else ws
+
+
+def _qk_gains(cfg, weights, device):
+    import torch
+    dtype = torch.bfloat16 if cfg.dtype == SBP_BF16 else torch.float32
+    for f in QK_NORM_FIELDS:
+        _is(weights[f], f, dtype, (cfg.head_dim,))
+        if weights[f].device != device:
+            raise ValueError(f"{f}: must be on {device}")
+    return QkGains(*[weights[f].data_ptr() for f in QK_NORM_FIELDS])
+
+
+def _layer_backward(reverse, cfg, weights, x, dy, dx, grads, ws, stream):
+    lib = load()
+    qk_norm = has_qk_norm(weights)
+    ws = _layer_ws(cfg, qk_norm, ws, x.device)
     w = _struct(LayerWeights, weights)
     g = _struct(LayerGrads, grads)
+    if qk_norm:
+        import torch
+        gains = _qk_gains(cfg, weights, x.device)
+        for f in QK_NORM_FIELDS:
+            if grads.get(f) is None:
+                raise ValueError(f"grads: {f} is missing")
+            _is(grads[f], f"grads[{f!r}]", torch.float32, (cfg.head_dim,))
+        _check(lib.sbp_decoder_layer_qk_norm_backward_stream(
+            C.byref(cfg), C.byref(w), C.byref(gains), _ptr(x), _ptr(dy), _ptr(dx), C.byref(g),
+            *[_ptr(grads[f]) for f in QK_NORM_FIELDS], int(reverse), _ptr(ws), ws.numel(),
+            _stream(stream)))
+        return ws
+    fn = (lib.sbp_decoder_layer_backward_stream_reverse if reverse
+          else lib.sbp_decoder_layer_backward_stream)
     _check(fn(C.byref(cfg), C.byref(w), _ptr(x), _ptr(dy), _ptr(dx), C.byref(g), _ptr(ws),
               ws.numel(), _stream(stream)))
     return ws
 
 
 def decoder_layer_backward(cfg: LayerCfg, weights, x, dy, dx, grads, ws=None, stream=None):
-    return _layer_backward(load().sbp_decoder_layer_backward_stream, cfg, weights, x, dy, dx,
-                           grads, ws, stream)
+    """The streamed backward of a layer.  Weights with q_norm_g and k_norm_g [head_dim] add the
+    per-head norms of queries and keys (include/sbp_step.h); grads then has both too."""
+    return _layer_backward(False, cfg, weights, x, dy, dx, grads, ws, stream)
 
 
 def decoder_layer_backward_reverse(cfg: LayerCfg, weights, x, dy, dx, grads, ws=None,
                                    stream=None):
     """The layer backward with the chunks visited from last to first."""
-    return _layer_backward(load().sbp_decoder_layer_backward_stream_reverse, cfg, weights, x, dy,
-                           dx, grads, ws, stream)
+    return _layer_backward(True, cfg, weights, x, dy, dx, grads, ws, stream)
 
 
 def decoder_layer_forward(cfg: LayerCfg, weights, x, y, ws=None, stream=None):
-    need = layer_workspace_size(cfg)
-    if need == 0:
-        raise SbpError(1, "invalid layer configuration")
-    if ws is None:
-        ws = workspace(need, x.device)
+    lib = load()
+    qk_norm = has_qk_norm(weights)
+    ws = _layer_ws(cfg, qk_norm, ws, x.device)
     w = _struct(LayerWeights, weights)
-    _check(load().sbp_decoder_layer_forward_stream(C.byref(cfg), C.byref(w), _ptr(x), _ptr(y),
-                                                   _ptr(ws), ws.numel(), _stream(stream)))
+    if qk_norm:
+        gains = _qk_gains(cfg, weights, x.device)
+        _check(lib.sbp_decoder_layer_qk_norm_forward_stream(
+            C.byref(cfg), C.byref(w), C.byref(gains), _ptr(x), _ptr(y), _ptr(ws), ws.numel(),
+            _stream(stream)))
+    else:
+        _check(lib.sbp_decoder_layer_forward_stream(C.byref(cfg), C.byref(w), _ptr(x), _ptr(y),
+                                                    _ptr(ws), ws.numel(), _stream(stream)))
     return ws
 
 

@@ -19,6 +19,7 @@ from . import sbp
 class StackResult:
     loss: object                # device fp32 [1]
     grads: Dict[str, object]    # lm_head, final_g, embed, layers: List[dict]
+    grad_norm: object = None    # device fp32 [1] where the gradients were clipped
 
 
 class Workspaces:
@@ -36,17 +37,25 @@ class Workspaces:
         return t
 
 
+def _layer_ws(cfg: sbp.LayerCfg, layers: List[dict], ws: Workspaces):
+    return ws.get("layer", sbp.layer_workspace_size(cfg, any(map(sbp.has_qk_norm, layers))))
+
+
 def stack_forward(cfg: sbp.LayerCfg, embed, layers: List[dict], final_g, ids, ws: Workspaces,
-                  stream=None):
+                  stream=None, embed_scale=None):
     """Embedding and L chunked layer forwards; returns the layer inputs (checkpoints), the
-    final-norm output and its rstd."""
+    final-norm output and its rstd.  `embed_scale` (optional) multiplies the embedding rows;
+    layers with q_norm_g and k_norm_g norm their queries and keys per head."""
     import torch
     dev = embed.device
     N = cfg.batch * cfg.seq_len
     d = cfg.d_model
     xs = [torch.empty(N, d, dtype=embed.dtype, device=dev)]
-    sbp.embedding_forward(ids, embed, xs[0], stream=stream)
-    lws = ws.get("layer", sbp.layer_workspace_size(cfg))
+    if embed_scale is None:
+        sbp.embedding_forward(ids, embed, xs[0], stream=stream)
+    else:
+        sbp.embedding_scaled_forward(ids, embed, embed_scale, xs[0], stream=stream)
+    lws = _layer_ws(cfg, layers, ws)
     for W in layers:
         y = torch.empty(N, d, dtype=embed.dtype, device=dev)
         sbp.decoder_layer_forward(cfg, W, xs[-1], y, ws=lws, stream=stream)
@@ -59,8 +68,9 @@ def stack_forward(cfg: sbp.LayerCfg, embed, layers: List[dict], final_g, ids, ws
 
 def stack_backward_from(cfg: sbp.LayerCfg, layers: List[dict], final_g, lm_w, ids, targets,
                         loss_weights, xs, hf, rstd, ws: Workspaces, grads=None, stream=None,
-                        on_final=None):
-    """The streamed backward of the stack from its checkpoints.  `grads` (optional) holds fp32
+                        on_final=None, embed_scale=None):
+    """The streamed backward of the stack from its checkpoints (with the `embed_scale` of its
+    forward).  `grads` (optional) holds fp32
     gradient buffers to accumulate into (the layout StackResult.grads uses); else fresh zeros.
     `on_final` (optional) is called with "head" once the LM-head and final-norm gradients are
     queued, "layer{l}" after layer l's backward and "embed" at the end: the points after which
@@ -82,7 +92,7 @@ def stack_backward_from(cfg: sbp.LayerCfg, layers: List[dict], final_g, lm_w, id
                          ws=ws.get("rms", 0), stream=stream)
     if on_final:
         on_final("head")
-    lws = ws.get("layer", sbp.layer_workspace_size(cfg))
+    lws = _layer_ws(cfg, layers, ws)
     dxn = dhf                                        # reuse the buffer: dhf is consumed
     for li in range(len(layers) - 1, -1, -1):
         sbp.decoder_layer_backward(cfg, layers[li], xs[li], dx, dxn, grads["layers"][li],
@@ -90,10 +100,30 @@ def stack_backward_from(cfg: sbp.LayerCfg, layers: List[dict], final_g, lm_w, id
         if on_final:
             on_final(f"layer{li}")
         dx, dxn = dxn, dx
-    sbp.embedding_backward(ids, dx, grads["embed"], ws=ws.get("embed", 0), stream=stream)
+    if embed_scale is None:
+        sbp.embedding_backward(ids, dx, grads["embed"], ws=ws.get("embed", 0), stream=stream)
+    else:
+        need = sbp.embedding_scaled_backward_workspace_size(ids.numel(), d,
+                                                            grads["embed"].shape[0])
+        sbp.embedding_scaled_backward(ids, dx, embed_scale, grads["embed"],
+                                      ws=ws.get("embed", need), stream=stream)
     if on_final:
         on_final("embed")
     return StackResult(loss, grads)
+
+
+def layer_fields(weights: dict):
+    """The weight names of a layer, with those of its query/key norms where it has them."""
+    return sbp.WEIGHT_FIELDS + (sbp.QK_NORM_FIELDS if sbp.has_qk_norm(weights) else ())
+
+
+def grad_tensors(grads: dict) -> List[object]:
+    """Every gradient tensor of the stack's gradient dict, in a fixed order: what
+    sbp.GradList, and with it the global norm and the clipping, takes."""
+    out = [grads[n] for n in ("embed", "lm_head", "final_g") if grads.get(n) is not None]
+    for g in grads["layers"]:
+        out += [t for t in g.values() if t is not None]
+    return out
 
 
 def zero_grads(layers, lm_w, final_g, dev, embed_shape=None):
@@ -101,29 +131,41 @@ def zero_grads(layers, lm_w, final_g, dev, embed_shape=None):
     g = {"lm_head": torch.zeros(lm_w.shape, dtype=torch.float32, device=dev),
          "final_g": torch.zeros(final_g.shape, dtype=torch.float32, device=dev),
          "layers": [{n: (torch.zeros(W[n].shape, dtype=torch.float32, device=dev)
-                         if W.get(n) is not None else None) for n in sbp.WEIGHT_FIELDS}
-                    for W in layers]}
+                         if W.get(n) is not None else None)
+                     for n in layer_fields(W)} for W in layers]}
     if embed_shape is not None:
         g["embed"] = torch.zeros(embed_shape, dtype=torch.float32, device=dev)
     return g
 
 
 def stack_backward(cfg: sbp.LayerCfg, embed, layers: List[dict], final_g, lm_w, ids, targets,
-                   loss_weights, stream=None, keep_workspace: dict | None = None) -> StackResult:
+                   loss_weights, stream=None, keep_workspace: dict | None = None,
+                   embed_scale=None, max_grad_norm=None) -> StackResult:
     """Forward (checkpoints only) and streamed backward of the whole stack.
     ids/targets int32 [B*T]; loss_weights fp32 [B*T]; weights on the device in cfg.dtype.
-    Returns the loss and fp32 gradients (freshly zeroed, then accumulated by the library)."""
+    Returns the loss and fp32 gradients (freshly zeroed, then accumulated by the library),
+    clipped in place to the global norm `max_grad_norm` where that is given; the norm before the
+    clipping is then in the result's grad_norm."""
     ws = Workspaces(embed.device)
     if keep_workspace is not None:
         ws.bufs = keep_workspace
-    xs, hf, rstd = stack_forward(cfg, embed, layers, final_g, ids, ws, stream=stream)
+    xs, hf, rstd = stack_forward(cfg, embed, layers, final_g, ids, ws, stream=stream,
+                                 embed_scale=embed_scale)
     grads = zero_grads(layers, lm_w, final_g, embed.device, embed_shape=embed.shape)
-    return stack_backward_from(cfg, layers, final_g, lm_w, ids, targets, loss_weights, xs, hf,
-                               rstd, ws, grads=grads, stream=stream)
+    res = stack_backward_from(cfg, layers, final_g, lm_w, ids, targets, loss_weights, xs, hf,
+                              rstd, ws, grads=grads, stream=stream, embed_scale=embed_scale)
+    if max_grad_norm is not None:
+        import torch
+        gl = sbp.GradList(grad_tensors(grads))
+        res.grad_norm = torch.empty(1, dtype=torch.float32, device=embed.device)
+        sbp.grad_clip_norm(gl, max_grad_norm, res.grad_norm, stream=stream,
+                           ws=ws.get("grad_norm", sbp.grad_norm_workspace_size(len(gl))))
+    return res
 
 
 def stack_dpo_step(cfg: sbp.LayerCfg, embed, layers: List[dict], final_g, lm_w, ids, targets,
-                   response_mask, ref_logp, beta: float, ws: Workspaces, grads=None, stream=None):
+                   response_mask, ref_logp, beta: float, ws: Workspaces, grads=None, stream=None,
+                   embed_scale=None):
     """One DPO step on 2P sequences laid out [chosen_0, rejected_0, ...] (include/sbp_dpo.h):
     the forward keeps the layer inputs, the streamed LM-head forward gives the per-token CE, the
     DPO loss and the per-token weights w_t = d loss / d CE_t follow, and the streamed backward
@@ -135,7 +177,8 @@ def stack_dpo_step(cfg: sbp.LayerCfg, embed, layers: List[dict], final_g, lm_w, 
     if B % 2:
         raise ValueError("DPO needs an even number of sequences (chosen, rejected pairs)")
     N = B * T
-    xs, hf, rstd = stack_forward(cfg, embed, layers, final_g, ids, ws, stream=stream)
+    xs, hf, rstd = stack_forward(cfg, embed, layers, final_g, ids, ws, stream=stream,
+                                 embed_scale=embed_scale)
     V, d = lm_w.shape
     token_ce = torch.empty(N, dtype=torch.float32, device=dev)
     cws = ws.get("lmhead", sbp.lmhead_ce_workspace_size(N, d, V, cfg.num_chunks,
@@ -149,5 +192,5 @@ def stack_dpo_step(cfg: sbp.LayerCfg, embed, layers: List[dict], final_g, lm_w, 
     if grads is None:
         grads = zero_grads(layers, lm_w, final_g, dev, embed_shape=embed.shape)
     r = stack_backward_from(cfg, layers, final_g, lm_w, ids, targets, w, xs, hf, rstd, ws,
-                            grads=grads, stream=stream)
+                            grads=grads, stream=stream, embed_scale=embed_scale)
     return StackResult(loss, r.grads)

@@ -160,3 +160,88 @@ def test_wrappers_refuse_before_the_library():
         sbp.GradList([torch.zeros(4, 4, dtype=f).t()])
     with pytest.raises(ValueError, match="no gradients"):
         sbp.grad_clip_norm([], 1.0, torch.zeros(1))
+
+
+def test_layer_qk_norm_refusals(lib):
+    cfg = sbp.layer_cfg(1, 256, 64, 4, 4, 16, 172, 1e-6, 1e4, sbp.SBP_F32, 4)
+    none = ("bq", "bk", "bv")
+    w = sbp.LayerWeights(**{n: (FAKE if n not in none else None) for n in sbp.WEIGHT_FIELDS})
+    g = sbp.LayerGrads(**{n: (FAKE if n not in none else None) for n in sbp.WEIGHT_FIELDS})
+    gains = sbp.QkGains(FAKE, FAKE)
+
+    def fwd(c=cfg, gains=C.byref(gains), x=FAKE, y=FAKE, ws=FAKE, wsb=OK_WS):
+        return lib.sbp_decoder_layer_qk_norm_forward_stream(C.byref(c), C.byref(w), gains, x, y,
+                                                            ws, wsb, None)
+
+    def bwd(c=cfg, gains=C.byref(gains), x=FAKE, dqg=FAKE, dkg=FAKE, ws=FAKE, wsb=OK_WS):
+        return lib.sbp_decoder_layer_qk_norm_backward_stream(
+            C.byref(c), C.byref(w), gains, x, FAKE, FAKE, C.byref(g), dqg, dkg, 0, ws, wsb, None)
+    for bad in (dict(gains=None), dict(gains=C.byref(sbp.QkGains(FAKE, None))),
+                dict(gains=C.byref(sbp.QkGains(FAKE + 2, FAKE))), dict(x=None),
+                dict(ws=FAKE + 16)):
+        assert fwd(**bad) == 1 and bwd(**bad) == 1, bad
+    assert bwd(dqg=None) == 1 and bwd(dkg=FAKE + 4) == 1 and fwd(y=None) == 1
+    size = lib.sbp_decoder_layer_qk_norm_workspace_size
+    plain = lib.sbp_decoder_layer_workspace_size(C.byref(cfg))
+    assert size(C.byref(cfg)) != plain and size(None) == 0
+    assert fwd(wsb=size(C.byref(cfg)) - 1) == 3 and bwd(wsb=size(C.byref(cfg)) - 1) == 3
+    odd = sbp.layer_cfg(1, 256, 64, 4, 4, 15, 172, 1e-6, 1e4, sbp.SBP_F32, 4)
+    assert fwd(c=odd) == 2 and size(C.byref(odd)) == 0
+    assert not sbp.has_qk_norm({"q_norm_g": None})
+    with pytest.raises(ValueError, match="both"):
+        sbp.has_qk_norm({"q_norm_g": 1})
+
+
+class _FakeGrads:
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+
+
+def _clip_worker(rank, world, port, q):
+    """clip_sharded's exchange with the kernels replaced by their definitions."""
+    import torch.distributed as dist
+    from memory_efficient_exact_chunk_b200 import dp
+    dist.init_process_group("gloo", init_method=f"tcp://127.0.0.1:{port}", rank=rank,
+                            world_size=world)
+    sbp.GradList = _FakeGrads
+    sbp.grad_sqsum = lambda g, out, ws=None: out.copy_(
+        sum(t.double().square().sum() for t in g.tensors).reshape(1))
+
+    def clip(g, sqsum, max_norm, norm_out=None):
+        norm_out.copy_(sqsum.sqrt())
+        for t in g.tensors:
+            t.mul_(min(1.0, max_norm / (float(sqsum.sqrt()) + 1e-6)))
+    sbp.grad_clip = clip
+    g = dp.ShardedGrads([("a", [("x", (10, 7))]), ("b", [("y", (300,))])], world, rank, "cpu")
+    gen = torch.Generator().manual_seed(rank)
+    before = []
+    for name in g.order:
+        g.out[name].normal_(generator=gen)
+        before.append(g.out[name].clone())
+    norm = dp.clip_sharded(g, 0.5)
+    q.put((rank, float(norm), [t.tolist() for t in before], [g.out[n].tolist() for n in g.order]))
+    dist.barrier()
+    dist.destroy_process_group()
+
+
+def test_clip_sharded_adds_the_ranks_sums():
+    import socket
+
+    import torch.multiprocessing as mp
+    with socket.socket() as s:
+        s.bind(("127.0.0.1", 0))
+        port = s.getsockname()[1]
+    ctx = mp.get_context("spawn")
+    q = ctx.Queue()
+    ps = [ctx.Process(target=_clip_worker, args=(r, 2, port, q)) for r in range(2)]
+    for p in ps:
+        p.start()
+    got = sorted(q.get(timeout=120) for _ in ps)
+    for p in ps:
+        p.join(timeout=60)
+        assert p.exitcode == 0
+    norm = sum(sum(v * v for v in t) for _, _, before, _ in got for t in before) ** 0.5
+    for _, n, before, after in got:
+        assert abs(n - norm) <= 1e-5 * norm
+        for b, a in zip(before, after):
+            assert all(abs(x * 0.5 / norm - y) <= 1e-5 for x, y in zip(b, a))
