@@ -56,6 +56,7 @@ sbp_status sbp_embedding_scaled_backward(int64_t rows, int64_t cols, int64_t voc
  * 16-byte aligned pointers, ld a multiple of 16 bytes and head_dim a multiple of 16 take the
  * vector path.  Inputs and outputs may be the same buffer (with the same ld); they must not
  * overlap in any other way.  n_kv_heads = 0 leaves the keys out (their pointers are not read).
+ * rows < 2^30, rows x heads < 2^31 (else SBP_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------------------------ */
 typedef struct {
   int64_t rows, n_heads, n_kv_heads, head_dim; /* head_dim even, <= 256                        */

@@ -6,6 +6,8 @@
 //   dg += sum u xh,   dx = rstd (g u - xh mean(xh g u)).
 // A head is read once into registers, so both directions move each element once; they are bound
 // by HBM (bf16: 4 bytes an element forward, 10 backward).
+#include <type_traits>
+
 #include "sbp_internal.cuh"
 
 namespace sbp {
@@ -13,7 +15,6 @@ namespace sbp {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxPairs = 4;   // pairs (j, j + hd / 2) of one lane: hd <= 256
 
 inline int64_t nblk(int64_t n, int64_t t) { return (n + t - 1) / t; }
 
@@ -21,11 +22,11 @@ struct RowMap {      // rows are below 2^30, so their division is a 32-bit one
   const int* positions;
   unsigned seq_len;
   int64_t pos0, table_len, k_T;
-  __device__ __forceinline__ int64_t pos(int64_t r) const {
+  __device__ __forceinline__ int64_t pos(int r) const {
     return positions ? (int64_t)positions[r] : pos0 + (unsigned)r % seq_len;
   }
   // row of the keys' output that row r goes to
-  __device__ __forceinline__ int64_t k_row(int64_t r) const {
+  __device__ __forceinline__ int64_t k_row(int r) const {
     const unsigned b = (unsigned)r / seq_len;
     return k_T > 0 ? b * k_T + pos0 + ((unsigned)r - b * seq_len) : r;
   }
@@ -45,25 +46,27 @@ struct Heads {        // one of the two tensors (queries or keys)
   int64_t lddx;
 };
 
-// ---------------------------------------------------------------- vector path
 // 1 << kLw lanes share a head (8 at head_dim 128; the next power of two where hd / 16 is none).
 // A lane holds 8 elements of the first half of a head and the 8 that they are rotated with, so
-// the rotation needs no exchange.  The 8 are neighbours (kWide: one 16-byte access in bf16), or
-// two groups of 4 a group of lanes apart: then the 16-byte accesses of neighbouring lanes to
-// fp32 values lie side by side too (with 8 neighbours they touch half of each sector twice).
-template <int kLw, bool kWide>
+// the rotation needs no exchange.  Which 8:
+//   kWide    neighbours: one 16-byte access in bf16
+//   kSplit   two groups of 4, a group of lanes apart: the 16-byte accesses of neighbouring lanes
+//            to fp32 values lie side by side too (8 neighbours touch half of each sector twice)
+//   kScalar  every (1 << kLw)-th element, one by one: any even head_dim, any alignment
+enum Layout { kWide, kSplit, kScalar };
+template <int kLw, Layout kL>
 struct Lanes {
   static constexpr int per = 32 >> kLw;     // heads of a warp
-  int sub;          // which of them
-  int j0, j1;       // first elements of the lane's two groups of 4 in either half
-  bool in0, in1;    // they lie in the head
-  __device__ __forceinline__ Lanes(int lane, int half) : sub(lane >> kLw) {
-    const int l = lane & ((1 << kLw) - 1);
-    j0 = kWide ? 8 * l : 4 * l;
-    j1 = kWide ? j0 + 4 : j0 + (4 << kLw);
-    in0 = j0 < half;
-    in1 = j1 < half;
+  int sub, l, half;                         // which of them, the lane in it
+  __device__ __forceinline__ Lanes(int lane, int half_)
+      : sub(lane >> kLw), l(lane & ((1 << kLw) - 1)), half(half_) {}
+  // the lane's e-th element of either half
+  __device__ __forceinline__ int at(int e) const {
+    if constexpr (kL == kWide) return 8 * l + e;
+    if constexpr (kL == kSplit) return 4 * l + e + (e < 4 ? 0 : (4 << kLw) - 4);
+    return l + (e << kLw);
   }
+  __device__ __forceinline__ bool in(int e) const { return at(e) < half; }
 };
 template <int kLw>
 __device__ __forceinline__ float lanes_sum(float v) {
@@ -109,140 +112,128 @@ __device__ __forceinline__ float total(F2 a) {
 // Four elements as they lie in memory, and as two pairs.
 template <typename T>
 struct alignas(4 * sizeof(T)) Pack {
-  unsigned w[sizeof(T)];
+  T v[4];
 };
 __device__ __forceinline__ void unpack(const Pack<__nv_bfloat16>& x, F2* f) {
+  const unsigned* w = reinterpret_cast<const unsigned*>(x.v);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    f[i] = f2(__uint_as_float(x.w[i] << 16), __uint_as_float(x.w[i] & 0xffff0000u));
+    f[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
 __device__ __forceinline__ void unpack(const Pack<float>& x, F2* f) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    f[i] = f2(__uint_as_float(x.w[2 * i]), __uint_as_float(x.w[2 * i + 1]));
+  f[0] = f2(x.v[0], x.v[1]);
+  f[1] = f2(x.v[2], x.v[3]);
 }
-__device__ __forceinline__ Pack<__nv_bfloat16> pack(const F2* f, __nv_bfloat16) {
-  Pack<__nv_bfloat16> x;
-  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(x.w);
+__device__ __forceinline__ void pack(const F2* f, Pack<__nv_bfloat16>& x) {
+  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(x.v);
 #pragma unroll
   for (int i = 0; i < 2; ++i) h[i] = __float22bfloat162_rn(pair(f[i]));
-  return x;
 }
-__device__ __forceinline__ Pack<float> pack(const F2* f, float) {
-  Pack<float> x;
+__device__ __forceinline__ void pack(const F2* f, Pack<float>& x) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    x.w[2 * i] = __float_as_uint(pair(f[i]).x);
-    x.w[2 * i + 1] = __float_as_uint(pair(f[i]).y);
+    x.v[2 * i] = pair(f[i]).x;
+    x.v[2 * i + 1] = pair(f[i]).y;
   }
-  return x;
 }
 
-// A lane's 8 elements of one half of a head.
+// A lane's 8 elements of one half of a head; zeros past the half's end.
 template <typename T>
-struct Eight {
+struct alignas(16) Eight {
   Pack<T> lo, hi;
 };
-template <typename T, int kLw, bool kWide>
-__device__ __forceinline__ Eight<T> load(const T* p, const Lanes<kLw, kWide>& ln) {
+template <typename T, int kLw, Layout kL>
+__device__ __forceinline__ Eight<T> load(const T* p, const Lanes<kLw, kL>& ln) {
   Eight<T> x = {};
-  if constexpr (kWide) {
-    if (ln.in0) *reinterpret_cast<uint4*>(&x) = *reinterpret_cast<const uint4*>(p + ln.j0);
+  if constexpr (kL == kWide && sizeof(T) == 2) {
+    if (ln.in(0)) *reinterpret_cast<uint4*>(&x) = *reinterpret_cast<const uint4*>(p + ln.at(0));
+  } else if constexpr (kL != kScalar) {
+    if (ln.in(0)) x.lo = *reinterpret_cast<const Pack<T>*>(p + ln.at(0));
+    if (ln.in(4)) x.hi = *reinterpret_cast<const Pack<T>*>(p + ln.at(4));
   } else {
-    if (ln.in0) x.lo = *reinterpret_cast<const Pack<T>*>(p + ln.j0);
-    if (ln.in1) x.hi = *reinterpret_cast<const Pack<T>*>(p + ln.j1);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (ln.in(e)) (e < 4 ? x.lo : x.hi).v[e & 3] = p[ln.at(e)];
   }
   return x;
-}
-// fp32 tables, whatever the lanes' layout
-template <int kLw, bool kWide>
-__device__ __forceinline__ void load_table(const float* p, const Lanes<kLw, kWide>& ln, F2 (&f)[4]) {
-  Eight<float> x = {};
-  if (ln.in0) x.lo = *reinterpret_cast<const Pack<float>*>(p + ln.j0);
-  if (ln.in1) x.hi = *reinterpret_cast<const Pack<float>*>(p + ln.j1);
-  unpack(x.lo, f);
-  unpack(x.hi, f + 2);
 }
 template <typename T>
 __device__ __forceinline__ void unpack(const Eight<T>& x, F2 (&f)[4]) {
   unpack(x.lo, f);
   unpack(x.hi, f + 2);
 }
-template <typename T, int kLw, bool kWide>
-__device__ __forceinline__ void store(T* p, const Lanes<kLw, kWide>& ln, const F2 (&f)[4]) {
+template <typename T, int kLw, Layout kL>
+__device__ __forceinline__ void store(T* p, const Lanes<kLw, kL>& ln, const F2 (&f)[4]) {
   Eight<T> x;
-  x.lo = pack(f, T());
-  x.hi = pack(f + 2, T());
-  if constexpr (kWide) {
-    if (ln.in0) *reinterpret_cast<uint4*>(p + ln.j0) = *reinterpret_cast<const uint4*>(&x);
+  pack(f, x.lo);
+  pack(f + 2, x.hi);
+  if constexpr (kL == kWide && sizeof(T) == 2) {
+    if (ln.in(0)) *reinterpret_cast<uint4*>(p + ln.at(0)) = *reinterpret_cast<const uint4*>(&x);
+  } else if constexpr (kL != kScalar) {
+    if (ln.in(0)) *reinterpret_cast<Pack<T>*>(p + ln.at(0)) = x.lo;
+    if (ln.in(4)) *reinterpret_cast<Pack<T>*>(p + ln.at(4)) = x.hi;
   } else {
-    if (ln.in0) *reinterpret_cast<Pack<T>*>(p + ln.j0) = x.lo;
-    if (ln.in1) *reinterpret_cast<Pack<T>*>(p + ln.j1) = x.hi;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (ln.in(e)) p[ln.at(e)] = (e < 4 ? x.lo : x.hi).v[e & 3];
   }
 }
 
-template <typename T>
-constexpr bool kFwdWide = sizeof(T) == 2;
-
-// A warp takes U x (heads per warp) heads of one row (2 x 4 in bf16 at head_dim 128), all of
-// their loads in flight together and held as they came until their turn; the warps of a CTA take
-// neighbouring items, which share the row's angles in L1.  Gain and angle are multiplied once per
-// row, so a pair costs y1 = rs (a (g c) - b (g' s)), y2 = rs (b (g' c) + a (g s)).
-template <typename T>
-constexpr int kFwdHeads = 4 / sizeof(T);
-template <typename T, int U, int kLw>
+// Forward.  The heads of all rows are one list; a warp takes U x per neighbours of it, all of
+// their loads in flight together and held as they came until their turn.  U = 2 where the
+// neighbours always lie in one row (4096 rows of 32 + 8 heads of 128: 19.3 us, 25 with U = 1).
+// Gain and angle are multiplied once per row, so a pair of elements costs
+//   y1 = rs (a (g c) - b (g' s)),  y2 = rs (b (g' c) + a (g s)).
+template <typename T, int U, int kLw, Layout kL>
 __global__ void __launch_bounds__(kThreads, 3)
-qk_fwd_vec_kernel(unsigned rows, int hd, float inv_hd, unsigned q_items, unsigned row_items, Heads<T> q,
-                  Heads<T> k, RowMap map, const float* __restrict__ cosb,
-                  const float* __restrict__ sinb, float eps) {
+qk_fwd_kernel(int rows, int hd, float inv_hd, unsigned q_warps, unsigned warps, Heads<T> q,
+              Heads<T> k, RowMap map, const float* __restrict__ cosb,
+              const float* __restrict__ sinb, float eps) {
   const int half = hd / 2;
-  const unsigned item = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const unsigned r = item / row_items;
-  unsigned it = item - r * row_items;
-  if (r >= rows) return;
-  const bool is_k = it >= q_items;
+  unsigned item = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (item >= warps) return;
+  const bool is_k = item >= q_warps;
   const Heads<T>& t = is_k ? k : q;
-  if (is_k) it -= q_items;
-  const Lanes<kLw, kFwdWide<T>> ln(threadIdx.x & 31, half);
-  const int h0 = it * U * ln.per + ln.sub, step = ln.per * hd;
-  const T* x = t.x + r * t.ldx + (int64_t)h0 * hd;
-  Eight<T> a[U], b[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (h0 + u * ln.per < t.n) {
-      a[u] = load(x + u * step, ln);
-      b[u] = load(x + u * step + half, ln);
-    } else {
-      a[u] = b[u] = Eight<T>{};
-    }
+  if (is_k) item -= q_warps;
+  const Lanes<kLw, kL> ln(threadIdx.x & 31, half);
+  // the lane's heads: h of row r, and with U = 2 also h + per of the same row
+  const unsigned first = item * (U * ln.per);
+  int r = first / (unsigned)t.n;
+  int h = first - (unsigned)r * t.n + ln.sub;
+  if (U == 1 && h >= t.n) {        // a division only where a row ends
+    const int more = (unsigned)h / (unsigned)t.n;
+    r += more;
+    h -= more * t.n;
   }
-  T* y = t.y + (is_k ? map.k_row(r) : r) * t.ldy + (int64_t)h0 * hd;
-  const int64_t p = map.pos(r);
-  F2 gc[4], gs[4], hc[4], hs[4];       // g c, -g' s, g' c, g s
-  if (p < 0 || p >= map.table_len) {   // the whole warp: it is the row's position
-#pragma unroll
-    for (int i = 0; i < 4; ++i) gc[i] = f2(0.f);
+  const bool in = U > 1 || r < rows;     // (with U = 2 the items divide the list evenly)
+  const int step = ln.per * hd;
+  Eight<T> a[U] = {}, b[U] = {};
+  if (in) {
+    const T* x = t.x + r * t.ldx + h * hd;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (h0 + u * ln.per < t.n) {
-        store(y + u * step, ln, gc);
-        store(y + u * step + half, ln, gc);
-      }
+      a[u] = load(x + u * step, ln);
+      b[u] = load(x + u * step + half, ln);
     }
-    return;
   }
-  F2 c[4], s[4];
-  load_table(cosb + p * half, ln, c);
-  load_table(sinb + p * half, ln, s);
-  unpack(load(t.g, ln), gc);
-  unpack(load(t.g + half, ln), hc);
+  const int64_t p = in ? map.pos(r) : -1;
+  const bool ok = p >= 0 && p < map.table_len;
+  F2 gc[4], gs[4], hc[4], hs[4];       // g c, -g' s, g' c, g s
+  if (ok) {
+    F2 c[4], s[4];
+    unpack(load(cosb + p * half, ln), c);
+    unpack(load(sinb + p * half, ln), s);
+    unpack(load(t.g, ln), gc);
+    unpack(load(t.g + half, ln), hc);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    hs[i] = gc[i] * s[i];
-    gs[i] = neg(hc[i] * s[i]);
-    gc[i] = gc[i] * c[i];
-    hc[i] = hc[i] * c[i];
+    for (int i = 0; i < 4; ++i) {
+      hs[i] = gc[i] * s[i];
+      gs[i] = neg(hc[i] * s[i]);
+      gc[i] = gc[i] * c[i];
+      hc[i] = hc[i] * c[i];
+    }
   }
+  T* y = in ? t.y + (is_k ? map.k_row(r) : r) * t.ldy + h * hd : nullptr;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     F2 fa[4], fb[4], s2 = f2(0.f);
@@ -251,69 +242,76 @@ qk_fwd_vec_kernel(unsigned rows, int hd, float inv_hd, unsigned q_items, unsigne
 #pragma unroll
     for (int i = 0; i < 4; ++i) s2 = fma2(fa[i], fa[i], fma2(fb[i], fb[i], s2));
     const F2 rs = f2(rsqrtf(fmaf(lanes_sum<kLw>(total(s2)), inv_hd, eps)));
-    if (h0 + u * ln.per >= t.n) continue;
-    F2 y1[4], y2[4];
+    if (ok) {
+      F2 y1[4], y2[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y1[i] = fma2(fa[i], gc[i], fb[i] * gs[i]) * rs;
-      y2[i] = fma2(fb[i], hc[i], fa[i] * hs[i]) * rs;
+      for (int i = 0; i < 4; ++i) {
+        y1[i] = fma2(fa[i], gc[i], fb[i] * gs[i]) * rs;
+        y2[i] = fma2(fb[i], hc[i], fa[i] * hs[i]) * rs;
+      }
+      store(y + u * step, ln, y1);
+      store(y + u * step + half, ln, y2);
+    } else if (in) {
+      const F2 zero[4] = {};
+      store(y + u * step, ln, zero);
+      store(y + u * step + half, ln, zero);
     }
-    store(y + u * step, ln, y1);
-    store(y + u * step + half, ln, y2);
   }
 }
 
-// Backward.  Blocks [0, q_blocks) take the queries, the others the keys.  Warps take items of
-// `per` heads of one row in turn and keep the gain gradient of their elements in registers; the
-// block's sum goes to partial[block].
-template <typename T, int kLw>
+// Backward.  Blocks [0, q_blocks) take the queries, the others the keys.  Warps take `per`
+// neighbours of the list of heads in turn and keep the gain gradient of their elements in
+// registers; the block's sum goes to partial[block].
+template <typename T, int kLw, Layout kL>
 __global__ void __launch_bounds__(kThreads, 2)
-qk_bwd_vec_kernel(int rows, int hd, float inv_hd, int q_blocks, Heads<T> q, Heads<T> k,
-                  RowMap map, const float* __restrict__ cosb, const float* __restrict__ sinb,
-                  float eps, float* __restrict__ partial) {
+qk_bwd_kernel(int rows, int hd, float inv_hd, int q_blocks, Heads<T> q, Heads<T> k, RowMap map,
+              const float* __restrict__ cosb, const float* __restrict__ sinb, float eps,
+              float* __restrict__ partial) {
   __shared__ float red[kWarps][256];
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, half = hd / 2;
   const bool is_k = (int)blockIdx.x >= q_blocks;
   const Heads<T>& t = is_k ? k : q;
-  const int first = (is_k ? blockIdx.x - q_blocks : blockIdx.x) * kWarps + wid;
-  const int stride = (is_k ? gridDim.x - q_blocks : q_blocks) * kWarps;
-  const Lanes<kLw, false> ln(lane, half);
-  // item `first`, and the step to the warp's next item, as row and item of the row
-  const int row_items = (t.n + ln.per - 1) / ln.per;
-  const int step_r = stride / row_items, step_it = stride - step_r * row_items;
-  int r = first / row_items, it = first - r * row_items;
+  const Lanes<kLw, kL> ln(lane, half);
+  const int warp = (is_k ? blockIdx.x - q_blocks : blockIdx.x) * kWarps + wid;
+  const int stride = (is_k ? gridDim.x - q_blocks : q_blocks) * kWarps * ln.per;
+  // the lane's first head, and the step to its next one, as row and head of the row
+  const int first = warp * ln.per + ln.sub, step_r = stride / t.n, step_h = stride - step_r * t.n;
+  int r = first / t.n, h = first - r * t.n;
   F2 ga[4], gb[4], da[4], db[4];
   unpack(load(t.g, ln), ga);
   unpack(load(t.g + half, ln), gb);
 #pragma unroll
   for (int i = 0; i < 4; ++i) da[i] = db[i] = f2(0.f);
-  while (r < rows) {
-    const int h = it * ln.per + ln.sub;
-    const int64_t p = map.pos(r);
-    const bool ok = p >= 0 && p < map.table_len, in = h < t.n;
+  while (__any_sync(0xffffffffu, r < rows)) {
+    const bool in = r < rows;
+    bool ok = false;
     F2 a[4], b[4], u[4], v[4], s2 = f2(0.f);
-    if (in && ok) {
-      const T* x = t.x + r * t.ldx + h * hd;
-      const float* dy = t.dy + r * t.lddy + h * hd;
-      const Eight<T> xa = load(x, ln), xb = load(x + half, ln);
-      const Eight<float> d1p = load(dy, ln), d2p = load(dy + half, ln);
-      F2 c[4], s[4], d1[4], d2[4];
-      load_table(cosb + p * half, ln, c);
-      load_table(sinb + p * half, ln, s);
-      unpack(xa, a);
-      unpack(xb, b);
-      unpack(d1p, d1);
-      unpack(d2p, d2);
+    if (in) {
+      const int64_t p = map.pos(r);
+      ok = p >= 0 && p < map.table_len;
+      if (ok) {
+        const T* x = t.x + r * t.ldx + h * hd;
+        const float* dy = t.dy + r * t.lddy + h * hd;
+        const Eight<T> xa = load(x, ln), xb = load(x + half, ln);
+        const Eight<float> d1p = load(dy, ln), d2p = load(dy + half, ln);
+        F2 c[4], s[4], d1[4], d2[4];
+        unpack(load(cosb + p * half, ln), c);
+        unpack(load(sinb + p * half, ln), s);
+        unpack(xa, a);
+        unpack(xb, b);
+        unpack(d1p, d1);
+        unpack(d2p, d2);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        u[i] = fma2(d1[i], c[i], d2[i] * s[i]);
-        v[i] = fma2(d2[i], c[i], neg(d1[i] * s[i]));
-        s2 = fma2(a[i], a[i], fma2(b[i], b[i], s2));
+        for (int i = 0; i < 4; ++i) {
+          u[i] = fma2(d1[i], c[i], d2[i] * s[i]);
+          v[i] = fma2(d2[i], c[i], neg(d1[i] * s[i]));
+          s2 = fma2(a[i], a[i], fma2(b[i], b[i], s2));
+        }
       }
     }
     const float rs = rsqrtf(fmaf(lanes_sum<kLw>(total(s2)), inv_hd, eps));
     F2 dot2 = f2(0.f);
-    if (in && ok) {
+    if (ok) {
       const F2 r2 = f2(rs);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -330,18 +328,21 @@ qk_bwd_vec_kernel(int rows, int hd, float inv_hd, int q_blocks, Heads<T> q, Head
     if (in) {
       float* dx = t.dx + r * t.lddx + h * hd;
       const F2 r2 = f2(rs), m = f2(-dot);
+      F2 o1[4] = {}, o2[4] = {};
+      if (ok) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        u[i] = ok ? fma2(a[i], m, u[i]) * r2 : f2(0.f);
-        v[i] = ok ? fma2(b[i], m, v[i]) * r2 : f2(0.f);
+        for (int i = 0; i < 4; ++i) {
+          o1[i] = fma2(a[i], m, u[i]) * r2;
+          o2[i] = fma2(b[i], m, v[i]) * r2;
+        }
       }
-      store(dx, ln, u);
-      store(dx + half, ln, v);
+      store(dx, ln, o1);
+      store(dx + half, ln, o2);
     }
     r += step_r;
-    it += step_it;
-    if (it >= row_items) {
-      it -= row_items;
+    h += step_h;
+    if (h >= t.n) {
+      h -= t.n;
       ++r;
     }
   }
@@ -349,19 +350,20 @@ qk_bwd_vec_kernel(int rows, int hd, float inv_hd, int q_blocks, Heads<T> q, Head
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float2 p = pair(da[i]), o = pair(db[i]);
-    #pragma unroll
+#pragma unroll
     for (int x = 1 << kLw; x < 32; x <<= 1) {
       p.x += __shfl_xor_sync(0xffffffffu, p.x, x);
       p.y += __shfl_xor_sync(0xffffffffu, p.y, x);
       o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
       o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
     }
-    const int j = (i < 2 ? ln.j0 : ln.j1) + 2 * (i & 1);
-    if (ln.sub == 0 && (i < 2 ? ln.in0 : ln.in1)) {
-      red[wid][j] = p.x;
-      red[wid][j + 1] = p.y;
-      red[wid][j + half] = o.x;
-      red[wid][j + half + 1] = o.y;
+    if (ln.sub == 0 && ln.in(2 * i)) {
+      red[wid][ln.at(2 * i)] = p.x;
+      red[wid][ln.at(2 * i) + half] = o.x;
+    }
+    if (ln.sub == 0 && ln.in(2 * i + 1)) {
+      red[wid][ln.at(2 * i + 1)] = p.y;
+      red[wid][ln.at(2 * i + 1) + half] = o.y;
     }
   }
   __syncthreads();
@@ -370,134 +372,6 @@ qk_bwd_vec_kernel(int rows, int hd, float inv_hd, int q_blocks, Heads<T> q, Head
 #pragma unroll
     for (int i = 1; i < kWarps; ++i) sum += red[i][col];
     partial[(int64_t)blockIdx.x * hd + col] = sum;
-  }
-}
-
-// ---------------------------------------------------------------- any even head_dim, any stride
-// One warp per (row, head); lane l holds the pairs l, l + 32, ...
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-qk_fwd_kernel(int64_t rows, int hd, Heads<T> q, Heads<T> k, RowMap map,
-              const float* __restrict__ cosb, const float* __restrict__ sinb, float eps) {
-  const int lane = threadIdx.x & 31, half = hd / 2;
-  const int64_t heads = q.n + k.n;
-  for (int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); item < rows * heads;
-       item += (int64_t)gridDim.x * kWarps) {
-  const int64_t r = item / heads;
-  int hh = (int)(item - r * heads);
-  const bool is_k = hh >= q.n;
-  const Heads<T>& t = is_k ? k : q;
-  if (is_k) hh -= q.n;
-  const T* x = t.x + r * t.ldx + (int64_t)hh * hd;
-  T* y = t.y + (is_k ? map.k_row(r) : r) * t.ldy + (int64_t)hh * hd;
-  const int64_t p = map.pos(r);
-  const bool ok = p >= 0 && p < map.table_len;
-  float a[kMaxPairs], b[kMaxPairs], ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMaxPairs; ++i) {
-    const int j = lane + 32 * i;
-    a[i] = j < half ? ld_f(x, j) : 0.f;
-    b[i] = j < half ? ld_f(x, j + half) : 0.f;
-    ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
-  }
-  const float rs = rsqrtf(warp_sum(ss) / (float)hd + eps);
-#pragma unroll
-  for (int i = 0; i < kMaxPairs; ++i) {
-    const int j = lane + 32 * i;
-    if (j >= half) continue;
-    float y1 = 0.f, y2 = 0.f;
-    if (ok) {
-      const float c = cosb[p * half + j], s = sinb[p * half + j];
-      const float n1 = a[i] * rs * ld_f(t.g, j), n2 = b[i] * rs * ld_f(t.g, j + half);
-      y1 = n1 * c - n2 * s;
-      y2 = n2 * c + n1 * s;
-    }
-    st_f(y, j, y1);
-    st_f(y, j + half, y2);
-  }
-  }
-}
-
-// Blocks [0, q_blocks) take the queries, the others the keys; a block's warps take (row, head)
-// items in turn, keep the gain gradient of their pairs in registers and leave the block's sum
-// in partial[block].
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-qk_bwd_kernel(int64_t rows, int hd, int q_blocks, Heads<T> q, Heads<T> k, RowMap map,
-              const float* __restrict__ cosb, const float* __restrict__ sinb, float eps,
-              float* __restrict__ partial) {
-  __shared__ float red[kWarps][256];
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, half = hd / 2;
-  const bool is_k = (int)blockIdx.x >= q_blocks;
-  const Heads<T>& t = is_k ? k : q;
-  const int64_t b0 = is_k ? blockIdx.x - q_blocks : blockIdx.x;
-  const int64_t nb = is_k ? gridDim.x - q_blocks : q_blocks;
-  float ga[kMaxPairs], gb[kMaxPairs], da[kMaxPairs], db[kMaxPairs];
-#pragma unroll
-  for (int i = 0; i < kMaxPairs; ++i) {
-    const int j = lane + 32 * i;
-    ga[i] = j < half ? ld_f(t.g, j) : 0.f;
-    gb[i] = j < half ? ld_f(t.g, j + half) : 0.f;
-    da[i] = db[i] = 0.f;
-  }
-  for (int64_t item = b0 * kWarps + wid; item < rows * t.n; item += nb * kWarps) {
-    const int64_t r = item / t.n, hh = item - r * t.n;
-    const T* x = t.x + r * t.ldx + hh * hd;
-    const float* dy = t.dy + r * t.lddy + hh * hd;
-    float* dx = t.dx + r * t.lddx + hh * hd;
-    const int64_t p = map.pos(r);
-    const bool ok = p >= 0 && p < map.table_len;
-    float a[kMaxPairs], b[kMaxPairs], u[kMaxPairs], v[kMaxPairs], ss = 0.f, dot = 0.f;
-#pragma unroll
-    for (int i = 0; i < kMaxPairs; ++i) {
-      const int j = lane + 32 * i;
-      a[i] = b[i] = u[i] = v[i] = 0.f;
-      if (j < half && ok) {
-        a[i] = ld_f(x, j);
-        b[i] = ld_f(x, j + half);
-        const float d1 = dy[j], d2 = dy[j + half];
-        const float c = cosb[p * half + j], s = sinb[p * half + j];
-        u[i] = d1 * c + d2 * s;
-        v[i] = d2 * c - d1 * s;
-      }
-      ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
-    }
-    const float rs = rsqrtf(warp_sum(ss) / (float)hd + eps);
-#pragma unroll
-    for (int i = 0; i < kMaxPairs; ++i) {
-      if (ok) {
-        a[i] *= rs;
-        b[i] *= rs;
-        da[i] = fmaf(u[i], a[i], da[i]);
-        db[i] = fmaf(v[i], b[i], db[i]);
-      }
-      u[i] *= ga[i];
-      v[i] *= gb[i];
-      dot = fmaf(a[i], u[i], fmaf(b[i], v[i], dot));
-    }
-    dot = warp_sum(dot) / (float)hd;
-#pragma unroll
-    for (int i = 0; i < kMaxPairs; ++i) {
-      const int j = lane + 32 * i;
-      if (j >= half) continue;
-      dx[j] = ok ? rs * (u[i] - a[i] * dot) : 0.f;
-      dx[j + half] = ok ? rs * (v[i] - b[i] * dot) : 0.f;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kMaxPairs; ++i) {
-    const int j = lane + 32 * i;
-    if (j < half) {
-      red[wid][j] = da[i];
-      red[wid][j + half] = db[i];
-    }
-  }
-  __syncthreads();
-  for (int c = threadIdx.x; c < hd; c += kThreads) {
-    float s = red[0][c];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) s += red[w][c];
-    partial[(int64_t)blockIdx.x * hd + c] = s;
   }
 }
 
@@ -523,11 +397,19 @@ qk_gain_kernel(int hd, int q_blocks, int blocks, const float* __restrict__ parti
   dst[c] += s;
 }
 
-// blocks of the backward for the queries and the keys, in proportion to their items; the cap is
-// two resident CTAs per SM, all in one wave
+// log2 of the lanes that share a head
+int lanes_log2(int64_t hd) {
+  int lw = 0;
+  while ((16 << lw) < hd) ++lw;
+  return lw;
+}
+
+// blocks of the backward for the queries and the keys, in proportion to their heads; at most two
+// resident CTAs per SM, all in one wave
+int max_blocks() { return sm_count() * 2; }
 void bwd_blocks(const QkNorm& a, int& qb, int& kb) {
-  const int64_t cap = (int64_t)sm_count() * 2;
-  const int64_t qi = nblk(a.rows * a.q.n, kWarps), ki = nblk(a.rows * a.k.n, kWarps);
+  const int64_t cap = max_blocks(), per = kWarps * (32 >> lanes_log2(a.hd));
+  const int64_t qi = nblk(a.rows * a.q.n, per), ki = nblk(a.rows * a.k.n, per);
   if (qi + ki <= cap) {
     qb = (int)qi;
     kb = (int)ki;
@@ -537,14 +419,7 @@ void bwd_blocks(const QkNorm& a, int& qb, int& kb) {
   }
 }
 
-// log2 of the lanes that share a head on the vector path
-int lanes_log2(int64_t hd) {
-  int lw = 0;
-  while ((16 << lw) < hd) ++lw;
-  return lw;
-}
-
-// whether the vector path takes this tensor (see qk_fwd_vec_kernel)
+// whether the tensor's rows keep accesses of four elements (eight: bf16 forward) aligned
 bool vec_ok(const QkNormHeads& h, int dt, bool backward) {
   auto al = [](const void* p) { return ((uintptr_t)p & 15) == 0; };
   if (h.n == 0) return true;
@@ -554,7 +429,8 @@ bool vec_ok(const QkNormHeads& h, int dt, bool backward) {
   return al(h.y) && h.ldy % unit == 0;
 }
 bool vec_ok(const QkNorm& a, bool backward) {
-  return a.hd % (a.dt == DT_BF16 && !backward ? 16 : 8) == 0 && vec_ok(a.q, a.dt, backward) && vec_ok(a.k, a.dt, backward);
+  return a.hd % (a.dt == DT_BF16 && !backward ? 16 : 8) == 0 && vec_ok(a.q, a.dt, backward) &&
+         vec_ok(a.k, a.dt, backward);
 }
 
 template <typename T>
@@ -567,83 +443,86 @@ RowMap map_of(const QkNorm& a) {
                 a.k_T};
 }
 
-template <typename T, int kLw>
-void launch_fwd_vec(const QkNorm& a, cudaStream_t st) {
-  constexpr int U = kFwdHeads<T>, per = U * (32 >> kLw);
-  const int64_t qi = nblk(a.q.n, per), ki = nblk(a.k.n, per);
-  launch(qk_fwd_vec_kernel<T, U, kLw>, dim3((unsigned)nblk(a.rows * (qi + ki), kWarps)),
-         dim3(kThreads), 0, st, (unsigned)a.rows, (int)a.hd, 1.f / a.hd, (unsigned)qi,
-         (unsigned)(qi + ki), heads_of<T>(a.q), heads_of<T>(a.k), map_of(a), a.cosb, a.sinb,
-         a.eps);
-}
-
-template <typename T, int kLw>
-void launch_bwd_vec(const QkNorm& a, int qb, int kb, float* partial, cudaStream_t st) {
-  launch(qk_bwd_vec_kernel<T, kLw>, dim3(qb + kb), dim3(kThreads), 0, st, (int)a.rows, (int)a.hd,
-         1.f / a.hd, qb, heads_of<T>(a.q), heads_of<T>(a.k), map_of(a), a.cosb, a.sinb, a.eps,
-         partial);
-}
-
-template <typename T>
-cudaError_t fwd(const QkNorm& a, cudaStream_t st) {
-  if (vec_ok(a, false)) {
-    switch (lanes_log2(a.hd)) {
-      case 0: launch_fwd_vec<T, 0>(a, st); break;
-      case 1: launch_fwd_vec<T, 1>(a, st); break;
-      case 2: launch_fwd_vec<T, 2>(a, st); break;
-      case 3: launch_fwd_vec<T, 3>(a, st); break;
-      default: launch_fwd_vec<T, 4>(a, st);
-    }
-    return cudaGetLastError();
-  }
-  const int64_t n = nblk(a.rows * (a.q.n + a.k.n), kWarps);
-  launch(qk_fwd_kernel<T>, dim3((unsigned)imin(n, (int64_t)sm_count() * 8)), dim3(kThreads), 0,
-         st, a.rows, (int)a.hd, heads_of<T>(a.q), heads_of<T>(a.k), map_of(a), a.cosb, a.sinb,
-         a.eps);
-  return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t bwd(const QkNorm& a, float* dq_g, float* dk_g, float* partial, cudaStream_t st) {
+struct Backward {
   int qb, kb;
-  bwd_blocks(a, qb, kb);
-  if (vec_ok(a, true)) {
-    switch (lanes_log2(a.hd)) {
-      case 0: launch_bwd_vec<T, 0>(a, qb, kb, partial, st); break;
-      case 1: launch_bwd_vec<T, 1>(a, qb, kb, partial, st); break;
-      case 2: launch_bwd_vec<T, 2>(a, qb, kb, partial, st); break;
-      case 3: launch_bwd_vec<T, 3>(a, qb, kb, partial, st); break;
-      default: launch_bwd_vec<T, 4>(a, qb, kb, partial, st);
-    }
-  } else {
-    launch(qk_bwd_kernel<T>, dim3(qb + kb), dim3(kThreads), 0, st, a.rows, (int)a.hd, qb,
-           heads_of<T>(a.q), heads_of<T>(a.k), map_of(a), a.cosb, a.sinb, a.eps, partial);
+  float* partial;
+};
+
+template <typename T, int U, int kLw, Layout kL>
+void launch_fwd_heads(const QkNorm& a, cudaStream_t st) {
+  constexpr int per = U * (32 >> kLw);
+  const int64_t qw = nblk(a.rows * a.q.n, per), kw = nblk(a.rows * a.k.n, per);
+  launch(qk_fwd_kernel<T, U, kLw, kL>, dim3((unsigned)nblk(qw + kw, kWarps)), dim3(kThreads), 0,
+         st, (int)a.rows, (int)a.hd, 1.f / a.hd, (unsigned)qw, (unsigned)(qw + kw),
+         heads_of<T>(a.q), heads_of<T>(a.k), map_of(a), a.cosb, a.sinb, a.eps);
+}
+
+template <typename T, int kLw, Layout kL>
+void launch_fwd(const QkNorm& a, const Backward&, cudaStream_t st) {
+  if constexpr (kL == kWide) {
+    constexpr int two = 2 * (32 >> kLw);
+    if (a.q.n % two == 0 && a.k.n % two == 0) return launch_fwd_heads<T, 2, kLw, kL>(a, st);
   }
-  launch(qk_gain_kernel, dim3((unsigned)nblk(a.hd, 32), kb ? 2 : 1), dim3(1024), 0, st,
-         (int)a.hd, qb, qb + kb, (const float*)partial, dq_g, dk_g);
-  return cudaGetLastError();
+  launch_fwd_heads<T, 1, kLw, kL>(a, st);
+}
+
+template <typename T, int kLw, Layout kL>
+void launch_bwd(const QkNorm& a, const Backward& b, cudaStream_t st) {
+  launch(qk_bwd_kernel<T, kLw, kL>, dim3(b.qb + b.kb), dim3(kThreads), 0, st, (int)a.rows,
+         (int)a.hd, 1.f / a.hd, b.qb, heads_of<T>(a.q), heads_of<T>(a.k), map_of(a), a.cosb,
+         a.sinb, a.eps, b.partial);
+}
+
+template <typename T, Layout kL, bool kBwd>
+void launch_width(const QkNorm& a, const Backward& b, cudaStream_t st) {
+  auto go = [&](auto lw) {
+    constexpr int kLw = decltype(lw)::value;
+    if constexpr (kBwd)
+      launch_bwd<T, kLw, kL>(a, b, st);
+    else
+      launch_fwd<T, kLw, kL>(a, b, st);
+  };
+  switch (lanes_log2(a.hd)) {
+    case 0: return go(std::integral_constant<int, 0>());
+    case 1: return go(std::integral_constant<int, 1>());
+    case 2: return go(std::integral_constant<int, 2>());
+    case 3: return go(std::integral_constant<int, 3>());
+    default: return go(std::integral_constant<int, 4>());
+  }
+}
+
+template <typename T, bool kBwd>
+void launch_type(const QkNorm& a, const Backward& b, cudaStream_t st) {
+  if (vec_ok(a, kBwd))
+    launch_width<T, sizeof(T) == 2 && !kBwd ? kWide : kSplit, kBwd>(a, b, st);
+  else
+    launch_width<T, kScalar, kBwd>(a, b, st);
 }
 
 }  // namespace
 
 cudaError_t qk_norm_rope_fwd(const QkNorm& a, cudaStream_t st) {
-  return a.dt == DT_BF16 ? fwd<__nv_bfloat16>(a, st) : fwd<float>(a, st);
+  if (a.dt == DT_BF16)
+    launch_type<__nv_bfloat16, false>(a, {}, st);
+  else
+    launch_type<float, false>(a, {}, st);
+  return cudaGetLastError();
 }
 
-size_t qk_norm_bwd_partial_floats(int64_t rows, int64_t n_heads, int64_t n_kv, int64_t hd) {
-  QkNorm a;
-  a.rows = rows;
-  a.q.n = n_heads;
-  a.k.n = n_kv;
-  int qb, kb;
-  bwd_blocks(a, qb, kb);
-  return (size_t)(qb + kb) * hd;
-}
+size_t qk_norm_bwd_partial_floats(int64_t hd) { return (size_t)max_blocks() * hd; }
 
 cudaError_t qk_norm_rope_bwd(const QkNorm& a, float* dq_g, float* dk_g, float* partial,
                              cudaStream_t st) {
-  return a.dt == DT_BF16 ? bwd<__nv_bfloat16>(a, dq_g, dk_g, partial, st)
-                         : bwd<float>(a, dq_g, dk_g, partial, st);
+  Backward b;
+  bwd_blocks(a, b.qb, b.kb);
+  b.partial = partial;
+  if (a.dt == DT_BF16)
+    launch_type<__nv_bfloat16, true>(a, b, st);
+  else
+    launch_type<float, true>(a, b, st);
+  launch(qk_gain_kernel, dim3((unsigned)nblk(a.hd, 32), b.kb ? 2 : 1), dim3(1024), 0, st,
+         (int)a.hd, b.qb, b.qb + b.kb, (const float*)partial, dq_g, dk_g);
+  return cudaGetLastError();
 }
 
 }  // namespace sbp

@@ -188,9 +188,7 @@ void layer_carve(Carver& c, const sbp_layer_cfg& L, LayerPlan& p, bool qk_norm =
     p.qraw = c.take_bytes((size_t)R * dq * es);
     p.kraw = c.take_bytes((size_t)R * dkv * es);
     p.vraw = c.take_bytes((size_t)R * dkv * es);
-    const size_t nq = qk_norm_bwd_partial_floats(R, L.n_heads, 0, L.head_dim);
-    const size_t nk = qk_norm_bwd_partial_floats(R, L.n_kv_heads, 0, L.head_dim);
-    p.gpart = c.take<float>(nq > nk ? nq : nk);
+    p.gpart = c.take<float>(qk_norm_bwd_partial_floats(L.head_dim));
   }
 }
 

@@ -394,7 +394,7 @@ struct QkNorm {
   int64_t k_T = 0;
 };
 cudaError_t qk_norm_rope_fwd(const QkNorm& a, cudaStream_t st);
-size_t qk_norm_bwd_partial_floats(int64_t rows, int64_t n_heads, int64_t n_kv, int64_t hd);
+size_t qk_norm_bwd_partial_floats(int64_t hd);
 cudaError_t qk_norm_rope_bwd(const QkNorm& a, float* dq_g, float* dk_g, float* partial,
                              cudaStream_t st);
 

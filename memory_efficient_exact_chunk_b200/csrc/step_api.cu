@@ -64,8 +64,10 @@ sbp_status check_qk(const sbp_qk_cfg* c) {
     return fail(SBP_ERR_INVALID_ARG, "rows, n_heads, head_dim and table_len must be positive");
   if (c->head_dim % 2 != 0 || c->head_dim > 256)
     return fail(SBP_ERR_UNSUPPORTED, "head_dim must be even and <= 256");
-  if (c->rows >= kMaxRows || c->n_heads > 65536 || c->n_kv_heads > 65536)
-    return fail(SBP_ERR_UNSUPPORTED, "rows must be below 2^30 and heads at most 65536");
+  if (c->rows >= kMaxRows || c->rows * imax(c->n_heads, c->n_kv_heads) >= 2 * kMaxRows ||
+      c->n_heads > 65536 || c->n_kv_heads > 65536)
+    return fail(SBP_ERR_UNSUPPORTED,
+                "rows must be below 2^30, heads at most 65536 and rows x heads below 2^31");
   if (c->dtype != SBP_F32 && c->dtype != SBP_BF16)
     return fail(SBP_ERR_INVALID_ARG, "unknown dtype %d", c->dtype);
   if (!(c->eps >= 0.f)) return fail(SBP_ERR_INVALID_ARG, "eps must be >= 0");
@@ -219,8 +221,7 @@ sbp_status sbp_qk_norm_rope_forward(const sbp_qk_cfg* cfg, const void* q, int64_
 
 size_t sbp_qk_norm_rope_backward_workspace_size(const sbp_qk_cfg* cfg) {
   if (check_qk(cfg) != SBP_OK) return 0;
-  return sizeof(float) *
-         qk_norm_bwd_partial_floats(cfg->rows, cfg->n_heads, cfg->n_kv_heads, cfg->head_dim);
+  return sizeof(float) * qk_norm_bwd_partial_floats(cfg->head_dim);
 }
 
 sbp_status sbp_qk_norm_rope_backward(const sbp_qk_cfg* cfg, const void* q, int64_t ldq,

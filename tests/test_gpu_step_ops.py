@@ -193,6 +193,9 @@ QK = [  # rows, heads, kv heads, head_dim, dtype, layout, positions
     (40, 5, 5, 210, "bf16", "fused", None), (900, 3, 1, 32, "bf16", "plain", 300),
     (9, 2, 1, 6, "f32", "odd", "outside"), (2050, 9, 3, 112, "f32", "plain", "any"),
     (3000, 1, 1, 64, "f32", "fused", None), (17, 64, 1, 48, "bf16", "plain", None),
+    (700, 1, 512, 16, "bf16", "plain", 700), (999, 1, 3, 8, "f32", "fused", "outside"),
+    (1500, 5, 2, 24, "bf16", "plain", "any"), (333, 3, 1, 256, "bf16", "fused", 111),
+    (2000, 7, 1, 102, "bf16", "fused", "any"), (600, 2, 2, 254, "f32", "plain", None),
 ]
 
 
