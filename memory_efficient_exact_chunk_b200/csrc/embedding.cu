@@ -36,6 +36,22 @@ int vec_width(int64_t cols, int es) {
   return v;
 }
 
+// n / d and n % d by a multiplication, for n and d below 2^31: the quotient by floor(2^32 / d) is
+// at most one short.
+struct Divisor {
+  unsigned d, m;
+  explicit Divisor(unsigned d_) : d(d_), m((unsigned)(((uint64_t)1 << 32) / d_ - (d_ == 1))) {}
+  __device__ __forceinline__ unsigned divide(unsigned n, unsigned& rest) const {
+    unsigned q = __umulhi(n, m);
+    rest = n - q * d;
+    if (rest >= d) {
+      rest -= d;
+      ++q;
+    }
+    return q;
+  }
+};
+
 // ---------------------------------------------------------------- forward
 // The rows are one list of cols / V vectors each; a CTA takes kFwdUnroll * 256 consecutive
 // vectors, so that a thread has kFwdUnroll independent loads in flight whatever the row length.
@@ -44,9 +60,10 @@ int vec_width(int64_t cols, int es) {
 constexpr int kFwdUnroll = 4;
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads)
-embed_scaled_fwd_kernel(int64_t rows, unsigned nv, int64_t vocab, float scale,
+embed_scaled_fwd_kernel(int64_t rows, Divisor by_nv, int64_t vocab, float scale,
                         const int* __restrict__ ids, const T* __restrict__ table,
                         T* __restrict__ y) {
+  const unsigned nv = by_nv.d;
   const int64_t first = (int64_t)blockIdx.x * (kFwdUnroll * kThreads);
   const int64_t r0 = first / nv;
   const unsigned o0 = (unsigned)(first - r0 * nv) + threadIdx.x;
@@ -56,11 +73,11 @@ embed_scaled_fwd_kernel(int64_t rows, unsigned nv, int64_t vocab, float scale,
   bool ok[kFwdUnroll];
 #pragma unroll
   for (int k = 0; k < kFwdUnroll; ++k) {
-    const unsigned o = o0 + k * kThreads, dr = o / nv;
-    const int64_t r = r0 + dr;
+    unsigned c;
+    const int64_t r = r0 + by_nv.divide(o0 + k * kThreads, c);
     const int64_t v = r < rows ? ids[r] : -1;
     ok[k] = v >= 0 && v < vocab;
-    if (ok[k]) x[k] = tv[v * nv + (o - dr * nv)];
+    if (ok[k]) x[k] = tv[v * nv + c];
   }
 #pragma unroll
   for (int k = 0; k < kFwdUnroll; ++k) {
@@ -72,45 +89,116 @@ embed_scaled_fwd_kernel(int64_t rows, unsigned nv, int64_t vocab, float scale,
   }
 }
 
+// Rows that no vector of 8 bytes fits (an odd number of elements, or 2 of bf16): y is still one
+// aligned array, so a thread writes 8 bytes of it with one access and gathers them one by one.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+embed_scaled_fwd_odd_kernel(int64_t n, Divisor by_cols, int64_t vocab, float scale,
+                            const int* __restrict__ ids, const T* __restrict__ table,
+                            T* __restrict__ y) {
+  constexpr int kV = 8 / sizeof(T);
+  const unsigned cols = by_cols.d;
+  const int64_t first = (int64_t)blockIdx.x * (kFwdUnroll * kThreads * kV);
+  const int64_t r0 = first / cols;
+  const unsigned c0 = (unsigned)(first - r0 * cols) + threadIdx.x * kV;
+  Vec<T, kV> x[kFwdUnroll];
+  bool ok[kFwdUnroll];
+#pragma unroll
+  for (int k = 0; k < kFwdUnroll; ++k) {
+    const int64_t i = first + (k * kThreads + threadIdx.x) * kV;
+    ok[k] = false;
+    if (i + kV > n) continue;
+    const unsigned o = c0 + k * kThreads * kV;
+    unsigned c;
+    const unsigned dr = by_cols.divide(o, c);
+    if (c + kV <= cols) {               // inside one row
+      const int64_t v = ids[r0 + dr];
+      ok[k] = v >= 0 && v < vocab;
+      const T* t = table + v * cols + c;
+      if (ok[k]) {
+#pragma unroll
+        for (int j = 0; j < kV; ++j) x[k].v[j] = t[j];
+      }
+    } else {                            // over a row's end
+      ok[k] = true;
+#pragma unroll
+      for (int j = 0; j < kV; ++j) {
+        unsigned cj;
+        const int64_t v = ids[r0 + by_cols.divide(o + j, cj)];
+        st_f(x[k].v, j, v >= 0 && v < vocab ? ld_f(table, v * cols + cj) : 0.f);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kFwdUnroll; ++k) {
+    const int64_t i = first + (k * kThreads + threadIdx.x) * kV;
+    if (i >= n) break;
+    if (i + kV <= n) {
+#pragma unroll
+      for (int j = 0; j < kV; ++j) st_f(x[k].v, j, ok[k] ? scale * ld_f(x[k].v, j) : 0.f);
+      *reinterpret_cast<Vec<T, kV>*>(y + i) = x[k];
+    } else {                            // the last elements
+      for (int64_t e = i; e < n; ++e) {
+        const int64_t r = e / cols, v = ids[r];
+        const bool in = v >= 0 && v < vocab;
+        st_f(y, e, in ? scale * ld_f(table, v * cols + (e - r * cols)) : 0.f);
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------- sort by id
 // What the accumulation reads of a sorted position: its row, and its run (the positions with the
 // same id): where it starts and how long it is, and the id.
 //   sorted[p] = {row, start, length, id},  p in [0, *n_valid); rows of ids outside [0, vocab)
 // are left out.
 
-// Few rows: the sorted position of every row by counting.  A run starts at the number of rows
-// with a smaller id, and a row stands behind the earlier rows of its own id.  Sixteen threads
-// share a row; the ids pass through shared memory.  rows^2 comparisons: 2 us at 4096 rows, where
-// the three launches of the digit sort below take longer.
-constexpr int64_t kRankRows = 4096;
+// Up to 4096 rows: the sorted position of every row by counting.  A run starts at the number of
+// rows with a smaller id, and a row stands behind the earlier rows of its own id.  Sixteen
+// threads share a row; the ids pass through shared memory, four at a time.  Rows before and
+// behind the CTA's own are counted apart, so two comparisons per id give all three numbers.
+// rows^2 comparisons: 4096 rows take 8 us, 6857 rows 16, as much as the digit sort below.
+constexpr int kRankRows = 4096;
 constexpr int kRankShare = 16, kRankPerCta = kThreads / kRankShare;
+static_assert(kRankPerCta == kRankShare, "each of a row's threads takes one of the CTA's rows");
 __global__ void __launch_bounds__(kThreads)
 embed_rank_kernel(int rows, int vocab, const int* __restrict__ ids, int4* __restrict__ sorted,
-                  int* __restrict__ n_valid) {
+                  int* __restrict__ n_valid, int* __restrict__ n_long) {
   __shared__ __align__(16) int key[kRankRows];
-  for (int i = threadIdx.x; i < rows; i += kThreads) {
-    const int v = ids[i];
+  const int rows4 = (rows + 3) / 4, padded = (rows + 15) / 16 * 16;
+  for (int i = threadIdx.x; i < padded; i += kThreads) {
+    const int v = i < rows ? ids[i] : -1;
     key[i] = v < 0 || v >= vocab ? vocab : v;
   }
   __syncthreads();
-  const int r = blockIdx.x * kRankPerCta + threadIdx.x / kRankShare;
+  const int r0 = blockIdx.x * kRankPerCta, own = threadIdx.x / kRankShare;
   const int part = threadIdx.x % kRankShare;
-  const int mine = r < rows ? key[r] : vocab;
-  int less = 0, equal = 0, before = 0;
+  const int mine = key[r0 + own];
+  const int4* key4 = reinterpret_cast<const int4*>(key);
+  auto count = [&](int i, int& less, int& upto) {
+    const int4 k = key4[i];
+    less += (k.x < mine) + (k.y < mine) + (k.z < mine) + (k.w < mine);
+    upto += (k.x <= mine) + (k.y <= mine) + (k.z <= mine) + (k.w <= mine);
+  };
+  int less = 0, upto = 0, rank = 0;
+  const int b = r0 / 4, e = b + kRankPerCta / 4;    // the CTA's own rows, in fours
 #pragma unroll 4
-  for (int i = part; i < rows; i += kRankShare) {
-    const int k = key[i];
-    less += k < mine;
-    equal += k == mine;
-    before += k == mine && i < r;
-  }
+  for (int i = part; i < b; i += kRankShare) count(i, less, upto);
+  rank = upto - less;
+#pragma unroll 4
+  for (int i = e + part; i < rows4; i += kRankShare) count(i, less, upto);
+  const int k = key[r0 + part];
+  less += k < mine;
+  upto += k <= mine;
+  rank += k == mine && part < own;
 #pragma unroll
   for (int o = 1; o < kRankShare; o <<= 1) {
     less += __shfl_xor_sync(0xffffffffu, less, o);
-    equal += __shfl_xor_sync(0xffffffffu, equal, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
+    upto += __shfl_xor_sync(0xffffffffu, upto, o);
+    rank += __shfl_xor_sync(0xffffffffu, rank, o);
   }
-  if (part == 0 && r < rows && mine < vocab) sorted[less + before] = make_int4(r, less, equal, mine);
+  if (part == 0 && mine < vocab)
+    sorted[less + rank] = make_int4(r0 + own, less, upto - less, mine);
   if (blockIdx.x == 0) {
     __shared__ int red[kThreads / 32];
     int n = 0;
@@ -121,6 +209,7 @@ embed_rank_kernel(int rows, int vocab, const int* __restrict__ ids, int4* __rest
     if (threadIdx.x == 0) {
       for (int w = 1; w < kThreads / 32; ++w) n += red[w];
       *n_valid = n;
+      n_long[0] = n_long[1] = 0;
     }
   }
 }
@@ -139,8 +228,9 @@ __device__ __forceinline__ bool valid_id(int v, int vocab) { return v >= 0 && v 
 // counts[block][bucket]
 __global__ void __launch_bounds__(kDealThreads)
 embed_count_kernel(int rows, int per_block, int vocab, const int* __restrict__ ids,
-                   int* __restrict__ counts) {
+                   int* __restrict__ counts, int* __restrict__ n_long) {
   __shared__ int hist[kBuckets];
+  if (blockIdx.x == 0 && threadIdx.x < 2) n_long[threadIdx.x] = 0;
   hist[threadIdx.x] = 0;
   __syncthreads();
   const int r0 = blockIdx.x * per_block, r1 = min(rows, r0 + per_block);
@@ -179,8 +269,15 @@ embed_deal_kernel(int rows, int per_block, int vocab, const int* __restrict__ id
   __shared__ int red[kDealWarps];
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int b = threadIdx.x;                      // one bucket per thread in the scans
+  const int per_warp = per_block / kDealWarps;    // per_block is a multiple of 512
+  const int r0 = blockIdx.x * per_block + wid * per_warp;
+  // the first 128 ids of the warp's piece (all of them up to 262144 rows), read at once
+  constexpr int kHeld = (int)kDealMinRows / kDealThreads;
+  int held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) held[i] = r0 + 32 * i + lane < rows ? ids[r0 + 32 * i + lane] : -1;
   int total = 0, before = 0;
-#pragma unroll 8
+#pragma unroll 16
   for (int k = 0; k < (int)gridDim.x; ++k) {
     const int c = counts[k * kBuckets + b];
     total += c;
@@ -194,28 +291,13 @@ embed_deal_kernel(int rows, int per_block, int vocab, const int* __restrict__ id
     if (b == kBuckets - 1) base[kBuckets] = start + total;
   }
   __syncthreads();
-  const int per_warp = per_block / kDealWarps;    // per_block is a multiple of 512
-  const int r0 = blockIdx.x * per_block + wid * per_warp;
-  for (int i = 0; i < per_warp; i += 32) {
-    const int r = r0 + i + lane;
-    const int v = r < rows ? ids[r] : -1;
+  auto tally = [&](int v) {
     const int key = valid_id(v, vocab) ? v % kBuckets : kBuckets;
     const unsigned same = __match_any_sync(0xffffffffu, key);
     if (key < kBuckets && (same & ((1u << lane) - 1)) == 0) hist[wid][key] += __popc(same);
     __syncwarp();
-  }
-  __syncthreads();
-  int at = start + before;
-#pragma unroll
-  for (int w = 0; w < kDealWarps; ++w) {
-    const int c = hist[w][b];
-    hist[w][b] = at;
-    at += c;
-  }
-  __syncthreads();
-  for (int i = 0; i < per_warp; i += 32) {
-    const int r = r0 + i + lane;
-    const int v = r < rows ? ids[r] : -1;
+  };
+  auto place = [&](int v, int r) {
     const int key = valid_id(v, vocab) ? v % kBuckets : kBuckets;
     const unsigned same = __match_any_sync(0xffffffffu, key);
     const int rank = __popc(same & ((1u << lane) - 1));
@@ -227,7 +309,24 @@ embed_deal_kernel(int rows, int per_block, int vocab, const int* __restrict__ id
       dealt[pos] = make_int2(v, r);
     }
     __syncwarp();
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) tally(held[i]);
+  for (int i = 32 * kHeld; i < per_warp; i += 32)
+    tally(r0 + i + lane < rows ? ids[r0 + i + lane] : -1);
+  __syncthreads();
+  int at = start + before;
+#pragma unroll
+  for (int w = 0; w < kDealWarps; ++w) {
+    const int c = hist[w][b];
+    hist[w][b] = at;
+    at += c;
   }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) place(held[i], r0 + 32 * i + lane);
+  for (int i = 32 * kHeld; i < per_warp; i += 32)
+    place(r0 + i + lane < rows ? ids[r0 + i + lane] : -1, r0 + i + lane);
 }
 
 // One CTA per bucket: a counting sort by bin = id / kBuckets with `warps` histograms.  Shared
@@ -297,14 +396,16 @@ embed_bucket_kernel(int vocab, int bins, int warps, const int* __restrict__ base
 }
 
 // ---------------------------------------------------------------- accumulate
-// A run is cut into units of kUnit rows counted from its start.  A group of `group` threads
+// A run is cut into units of `unit` rows counted from its start.  A group of `group` threads
 // takes `window` consecutive sorted positions and adds every unit that begins there, all of its
 // rows in order, V columns per thread.  The unit of a run of one unit goes into the table; those
-// of longer runs go to partial rows, which embed_join_kernel adds in order.  In the list of
-// partial rows at most two units begin within kUnit positions: one that continues a run and one
-// that begins the next (a run longer than kUnit leaves room for no third), which gives the slot
-// 2 (p / kUnit) + (p is its run's start).
-constexpr int kUnit = 64;
+// of longer runs go to partial rows, which embed_join_kernel adds in order (the runs' starts are
+// left in two lists for it, in no particular order: the few of more than kLongUnits units from
+// the back).  In the list of
+// partial rows at most two units begin within `unit` positions: one that continues a run and one
+// that begins the next (a run longer than a unit leaves room for no third), which gives the slot
+// 2 (p / unit) + (p is its run's start).
+constexpr int kMaxUnit = 64, kMinUnit = 8, kLongUnits = 8;
 
 template <int V>
 __device__ __forceinline__ void vload(const float* p, float (&x)[V]) {
@@ -324,7 +425,7 @@ struct AccumArgs {
   int64_t cols;
   int rows, vocab;
   float scale;
-  int accumulate, group, window;
+  int accumulate, group, window, unit, clear_rows;
   int64_t acc_blocks;      // CTAs that accumulate; the ones behind them clear absent rows
   const int4* sorted;
   const int* n_valid;
@@ -332,31 +433,34 @@ struct AccumArgs {
   const unsigned char* present;
   const float* dy;
   float *d_table, *partial;
+  int *n_long, *longs, max_longs;     // n_long[0], n_long[1]: entries of the two lists
 };
 
 // The CTAs behind the accumulating ones clear the table rows whose id does not occur, in pieces
 // dealt in turn: by the flags of the sort, or by marking the few ids in shared memory.  Many
-// short CTAs write faster than few long ones (2.2 GB: 8 per SM 428 us, 64 per SM 393).
-constexpr int kClearRows = 16, kClearPerSm = 64;
+// short CTAs write faster than few long ones (2.2 GB: 8 per SM 428 us, 64 per SM 393); a piece
+// holds at least 64 KB, so that its marking costs little beside it.
+constexpr int kClearRows = 512, kClearPerSm = 64;
 template <int V>
 __device__ void clear_absent(const AccumArgs& a, int64_t b, int64_t nb) {
   __shared__ unsigned char here[kClearRows];
   const int64_t nv = a.cols / V;
+  const int piece = a.clear_rows;
   const float zero[V] = {};
-  for (int64_t v0 = b * kClearRows; v0 < a.vocab; v0 += nb * kClearRows) {
-    const int n = (int)imin(kClearRows, a.vocab - v0);
+  for (int64_t v0 = b * piece; v0 < a.vocab; v0 += nb * piece) {
+    const int n = (int)imin(piece, a.vocab - v0);
     __syncthreads();
-    if ((int)threadIdx.x < n) here[threadIdx.x] = a.ids ? 0 : a.present[v0 + threadIdx.x];
+    for (int i = threadIdx.x; i < n; i += blockDim.x) here[i] = a.ids ? 0 : a.present[v0 + i];
     __syncthreads();
     if (a.ids) {
-      for (int i = threadIdx.x; i < a.rows; i += kThreads) {
+      for (int i = threadIdx.x; i < a.rows; i += blockDim.x) {
         const int64_t v = a.ids[i] - v0;
         if (v >= 0 && v < n) here[v] = 1;
       }
       __syncthreads();
     }
     // a warp per row: its lanes write the row's vectors side by side
-    for (int i = threadIdx.x / 32; i < n; i += kThreads / 32) {
+    for (int i = threadIdx.x / 32; i < n; i += blockDim.x / 32) {
       if (here[i]) continue;
       float* d = a.d_table + (v0 + i) * a.cols;
       for (int64_t c = threadIdx.x % 32; c < nv; c += 32) vstore<V>(d + c * V, zero);
@@ -388,40 +492,59 @@ embed_accum_kernel(AccumArgs a) {
     return;
   }
   const int64_t c = ((int64_t)blockIdx.y * a.group + threadIdx.x % a.group) * V;
-  const int g = threadIdx.x / a.group, groups = kThreads / a.group;
+  const int g = threadIdx.x / a.group, groups = blockDim.x / a.group;
   const int n = *a.n_valid;
   const int64_t p0 = ((int64_t)blockIdx.x * groups + g) * a.window;
   const int p1 = (int)imin(n, p0 + a.window);
-  if (c >= a.cols) return;
-  for (int p = (int)imin(n, p0); p < p1; ++p) {
-    const int4 s = a.sorted[p];
-    if ((p - s.y) % kUnit != 0) continue;
-    const int e = min(p + kUnit, s.y + s.z);
-    float sum[V];
-    vload<V>(a.dy + (int64_t)s.x * a.cols + c, sum);
-    int i = p + 1;
-    for (; i + 4 <= e; i += 4) {
-      float x[4][V];
+  if (c >= a.cols || p0 >= p1) return;
+  // positions [b, e): the units that begin in the window, the last of them to its end
+  const int4 s0 = a.sorted[p0], s1 = a.sorted[p1 - 1];
+  const int into = ((int)p0 - s0.y) & (a.unit - 1);
+  const int b = into ? min((int)p0 + a.unit - into, s0.y + s0.z) : (int)p0;
+  if (b >= p1) return;
+  const int last = p1 - 1 - ((p1 - 1 - s1.y) & (a.unit - 1));
+  const int e = min(last + a.unit, s1.y + s1.z);
+  float sum[V];
+  int4 run;             // of the unit in hand, and where the unit begins
+  int from = b;
+  auto flush = [&]() {
+    if (run.z <= a.unit) {
+      put_row<V>(a, run.w, c, sum);
+      return;
+    }
+    vstore<V>(a.partial + (2 * (int64_t)(from / a.unit) + (from == run.y)) * a.cols + c, sum);
+    if (from == run.y && c == 0) {
+      if (run.z <= a.unit * kLongUnits)
+        a.longs[atomicAdd(a.n_long, 1)] = from;
+      else
+        a.longs[a.max_longs - 1 - atomicAdd(a.n_long + 1, 1)] = from;
+    }
+  };
+  // several rows in flight, whatever units they belong to
+  constexpr int kRows = V == 4 ? 4 : 8;
+  for (int p = b; p < e; p += kRows) {
+    int4 s[kRows];
+    float x[kRows][V];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) vload<V>(a.dy + (int64_t)a.sorted[i + k].x * a.cols + c, x[k]);
+    for (int k = 0; k < kRows; ++k) s[k] = a.sorted[min(p + k, e - 1)];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < kRows; ++k) vload<V>(a.dy + (int64_t)s[k].x * a.cols + c, x[k]);
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (p + k >= e) break;
+      if (((p + k - s[k].y) & (a.unit - 1)) == 0) {
+        if (p + k > b) flush();
+        run = s[k];
+        from = p + k;
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum[j] = x[k][j];
+      } else {
 #pragma unroll
         for (int j = 0; j < V; ++j) sum[j] += x[k][j];
-    }
-    for (; i < e; ++i) {
-      float x[V];
-      vload<V>(a.dy + (int64_t)a.sorted[i].x * a.cols + c, x);
-#pragma unroll
-      for (int j = 0; j < V; ++j) sum[j] += x[j];
-    }
-    if (s.z > kUnit) {
-      const int64_t slot = 2 * (int64_t)(p / kUnit) + (p == s.y);
-      vstore<V>(a.partial + slot * a.cols + c, sum);
-    } else {
-      put_row<V>(a, s.w, c, sum);
+      }
     }
   }
+  flush();
 }
 
 // At most kFewRows rows: no sort.  A warp takes (row, 32 V columns); it marks the rows of the
@@ -471,76 +594,81 @@ embed_few_kernel(AccumArgs a, int slabs) {
   put_row<V>(a, mine, c, sum);
 }
 
-// Runs longer than kUnit.  Each warp of CTA x looks through kUnit positions for the run longer
-// than kUnit that starts there (at most one does).  The CTA then takes the runs found one after
-// the other: its warps add an eighth of the run's partial rows each, V columns per lane, and
-// warp 0 joins the eight sums in order; CTA y takes every gridDim.y-th slab of columns.
+// Runs longer than a unit, by the lists: a warp takes (run, 32 V columns) and adds the run's
+// partial rows in order, V columns per lane.  Of runs of more than kLongUnits units a whole CTA
+// takes it: each warp adds an eighth of the units, warp 0 the eight sums.
 template <int V>
 __global__ void __launch_bounds__(kThreads)
 embed_join_kernel(AccumArgs a) {
   constexpr int kWarps = kThreads / 32;
   __shared__ float sums[kWarps][32 * V];
-  __shared__ int found[kWarps];
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int n = *a.n_valid;
-  const int64_t p0 = ((int64_t)blockIdx.x * kWarps + wid) * kUnit;
-  int at = -1;
+  const int slabs = (int)((a.cols + 32 * V - 1) / (32 * V));
+  // units [u0, u1) of the run that starts at `start`, eight of them in flight
+  auto add = [&](int start, int u0, int u1, int64_t c, float (&sum)[V]) {
+    const float* first = a.partial + 2 * (int64_t)(start / a.unit) * a.cols + c;
+    for (int u = u0; u < u1; u += 8) {
+      float x[8][V] = {};
 #pragma unroll
-  for (int k = 0; k < kUnit; k += 32) {
-    const int64_t p = p0 + k + lane;
-    bool is = false;
-    if (p < n) {
-      const int4 s = a.sorted[p];
-      is = s.y == p && s.z > kUnit;
+      for (int k = 0; k < 8; ++k)
+        if (u + k < u1) vload<V>(first + (2 * (int64_t)(u + k) + (u + k == 0)) * a.cols, x[k]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum[j] += x[k][j];
     }
-    const unsigned m = __ballot_sync(0xffffffffu, is);
-    if (m) at = (int)p0 + k + __ffs(m) - 1;
+  };
+  const int64_t items = (int64_t)a.n_long[0] * slabs, heavy = (int64_t)a.n_long[1] * slabs;
+  for (int64_t i = (int64_t)blockIdx.x * kWarps + wid; i < items; i += (int64_t)gridDim.x * kWarps) {
+    const int64_t run = i / slabs, c = ((i - run * slabs) * 32 + lane) * V;
+    const int4 s = a.sorted[a.longs[run]];
+    if (c >= a.cols) continue;
+    float sum[V] = {};
+    add(s.y, 0, (s.z + a.unit - 1) / a.unit, c, sum);
+    put_row<V>(a, s.w, c, sum);
   }
-  if (lane == 0) found[wid] = at;
-  __syncthreads();
-  for (int f = 0; f < kWarps; ++f) {
-    if (found[f] < 0) continue;
-    const int4 s = a.sorted[found[f]];
-    const int units = (s.z + kUnit - 1) / kUnit;
-    const int per = (units + kWarps - 1) / kWarps;
-    const int u0 = min(units, wid * per), u1 = min(units, u0 + per);
-    for (int64_t slab = blockIdx.y; slab * 32 * V < a.cols; slab += gridDim.y) {
-      const int64_t c = (slab * 32 + lane) * V;
-      float sum[V] = {};
-      if (c < a.cols) {
-#pragma unroll 8
-        for (int u = u0; u < u1; ++u) {
-          const int p = s.y + u * kUnit;
-          float x[V];
-          vload<V>(a.partial + (2 * (int64_t)(p / kUnit) + (u == 0)) * a.cols + c, x);
+  for (int64_t i = blockIdx.x; i < heavy; i += gridDim.x) {
+    const int64_t run = i / slabs, c = ((i - run * slabs) * 32 + lane) * V;
+    const int4 s = a.sorted[a.longs[a.max_longs - 1 - run]];
+    const int units = (s.z + a.unit - 1) / a.unit, per = (units + kWarps - 1) / kWarps;
+    float sum[V] = {};
+    if (c < a.cols) add(s.y, min(units, wid * per), min(units, wid * per + per), c, sum);
+    __syncthreads();
 #pragma unroll
-          for (int j = 0; j < V; ++j) sum[j] += x[j];
-        }
-      }
-      __syncthreads();
+    for (int j = 0; j < V; ++j) sums[wid][lane * V + j] = sum[j];
+    __syncthreads();
+    if (wid == 0 && c < a.cols) {
+      for (int w = 1; w < kWarps; ++w)
 #pragma unroll
-      for (int j = 0; j < V; ++j) sums[wid][lane * V + j] = sum[j];
-      __syncthreads();
-      if (wid == 0 && c < a.cols) {
-        for (int w = 1; w < kWarps; ++w)
-#pragma unroll
-          for (int j = 0; j < V; ++j) sum[j] += sums[w][lane * V + j];
-        put_row<V>(a, s.w, c, sum);
-      }
+        for (int j = 0; j < V; ++j) sum[j] += sums[w][lane * V + j];
+      put_row<V>(a, s.w, c, sum);
     }
   }
 }
 
 // ---------------------------------------------------------------- workspace
 struct Plan {
-  int* head;                // number of valid rows, or the buckets' starts with it behind them
+  int* head;                // number of valid rows, or the buckets' starts with it behind them,
+                            // and the entries of the lists of long runs
   int4* sorted;
   unsigned char* present;
   int2* dealt;
   int* counts;
   float* partial;
+  int* longs;
+  int64_t max_longs;
   size_t bytes;
 };
+
+// Rows of a unit: long units write few partial rows, short ones leave few sums in a row for a
+// group to wait for; a power of two that gives every SM sixteen groups' worth of full units
+// (6857 rows of 1312: 8, 13.9 us for the accumulation, 19.6 with 64; 64K rows of 4096: 64).
+int unit_rows(int64_t rows, int64_t cols) {
+  const int64_t slabs = nblk(cols, kThreads * vec_width(cols, 4));
+  int unit = kMinUnit;
+  while (unit < kMaxUnit && rows * slabs >= (int64_t)sm_count() * 16 * 2 * unit) unit *= 2;
+  return unit;
+}
 
 int64_t deal_rows(int64_t rows) {     // rows of a block of the deal, a multiple of 512
   const int64_t r = nblk(rows, kDealMaxBlocks);
@@ -555,15 +683,17 @@ Plan plan(void* ws, int64_t rows, int64_t cols, int64_t vocab) {
     off += (n + 255) & ~size_t(255);
     return q;
   };
-  p.head = static_cast<int*>(take(sizeof(int) * (kBuckets + 1)));
+  p.head = static_cast<int*>(take(sizeof(int) * (kBuckets + 3)));
   p.sorted = static_cast<int4*>(take(sizeof(int4) * rows));
   const bool deal = rows > kRankRows;
   p.present = static_cast<unsigned char*>(take(deal ? vocab : 0));
   p.dealt = static_cast<int2*>(take(deal ? sizeof(int2) * rows : 0));
   p.counts =
       static_cast<int*>(take(deal ? sizeof(int) * kBuckets * nblk(rows, deal_rows(rows)) : 0));
-  p.partial = static_cast<float*>(
-      take(rows > kUnit ? sizeof(float) * 2 * nblk(rows, kUnit) * cols : 0));
+  const int64_t units = rows > kFewRows ? nblk(rows, unit_rows(rows, cols)) : 0;
+  p.partial = static_cast<float*>(take(sizeof(float) * 2 * units * cols));
+  p.longs = static_cast<int*>(take(sizeof(int) * units));
+  p.max_longs = units;
   p.bytes = off;
   return p;
 }
@@ -573,42 +703,54 @@ cudaError_t fwd(int64_t rows, int64_t cols, int64_t vocab, float scale, const in
                 const void* table, void* y, cudaStream_t st) {
   const int64_t nv = cols / V;
   launch(embed_scaled_fwd_kernel<T, V>, dim3((unsigned)nblk(rows * nv, kFwdUnroll * kThreads)),
-         dim3(kThreads), 0, st, rows, (unsigned)nv, vocab, scale, ids,
+         dim3(kThreads), 0, st, rows, Divisor((unsigned)nv), vocab, scale, ids,
          static_cast<const T*>(table), static_cast<T*>(y));
   return cudaGetLastError();
 }
 
+template <typename T>
+cudaError_t fwd_odd(int64_t rows, int64_t cols, int64_t vocab, float scale, const int* ids,
+                    const void* table, void* y, cudaStream_t st) {
+  constexpr int64_t per = kFwdUnroll * kThreads * (8 / sizeof(T));
+  launch(embed_scaled_fwd_odd_kernel<T>, dim3((unsigned)nblk(rows * cols, per)), dim3(kThreads),
+         0, st, rows * cols, Divisor((unsigned)cols), vocab, scale, ids, static_cast<const T*>(table),
+         static_cast<T*>(y));
+  return cudaGetLastError();
+}
+
 // CTAs that clear absent rows
-int64_t clear_blocks(const AccumArgs& a) {
-  return a.accumulate ? 0 : imin(nblk(a.vocab, kClearRows), (int64_t)sm_count() * kClearPerSm);
+int64_t clear_blocks(AccumArgs& a) {
+  a.clear_rows = (int)imax(16, imin(kClearRows, 16384 / a.cols));
+  return a.accumulate ? 0 : imin(nblk(a.vocab, a.clear_rows), (int64_t)sm_count() * kClearPerSm);
 }
 
 template <int V>
 cudaError_t accum_few(AccumArgs a, cudaStream_t st) {
   const int64_t slabs = nblk(a.cols, 32 * V);
   a.acc_blocks = nblk(a.rows * slabs, kThreads / 32);
-  launch(embed_few_kernel<V>, dim3((unsigned)(a.acc_blocks + clear_blocks(a))), dim3(kThreads), 0,
-         st, a, (int)slabs);
+  const int64_t clear = clear_blocks(a);
+  launch(embed_few_kernel<V>, dim3((unsigned)(a.acc_blocks + clear)), dim3(kThreads), 0, st, a,
+         (int)slabs);
   return cudaGetLastError();
 }
 
 template <int V>
 cudaError_t accum(AccumArgs a, cudaStream_t st) {
   const int64_t nv = a.cols / V;
-  a.group = 8;
-  while (a.group < kThreads && a.group < nv) a.group *= 2;
+  // the columns in equal slabs of at most 256 vectors; a group of whole warps takes one (of 8 or
+  // 16 threads where a row is shorter than a warp), a CTA as many groups as 256 threads hold
+  const int64_t slabs = nblk(nv, kThreads);
+  a.group = nv <= 8 ? 8 : nv <= 16 ? 16 : (int)nblk(nblk(nv, slabs), 32) * 32;
   const int groups = kThreads / a.group;
-  const int64_t slabs = nblk(nv, a.group);
   // positions per group: as many as leave every SM sixteen CTAs' worth of groups
   const int64_t fill = (int64_t)sm_count() * 16 * groups;
   a.window = (int)imax(1, imin(32, a.rows * slabs / fill));
   a.acc_blocks = nblk(nblk(a.rows, a.window), groups);
-  launch(embed_accum_kernel<V>,
-         dim3((unsigned)(a.acc_blocks + clear_blocks(a)), (unsigned)slabs), dim3(kThreads), 0, st,
-         a);
-  launch(embed_join_kernel<V>,
-         dim3((unsigned)nblk(a.rows, kUnit * (kThreads / 32)), (unsigned)imin(nblk(nv, 32), 16)),
-         dim3(kThreads), 0, st, a);
+  const int64_t clear = clear_blocks(a);
+  a.unit = unit_rows(a.rows, a.cols);
+  launch(embed_accum_kernel<V>, dim3((unsigned)(a.acc_blocks + clear), (unsigned)slabs),
+         dim3(a.group * groups), 0, st, a);
+  launch(embed_join_kernel<V>, dim3(sm_count() * 4), dim3(kThreads), 0, st, a);
   return cudaGetLastError();
 }
 
@@ -619,14 +761,14 @@ cudaError_t sort_by_id(int64_t rows, int64_t vocab, const int* ids, const Plan& 
   a.n_valid = p.head;
   if (rows <= kRankRows) {
     launch(embed_rank_kernel, dim3((unsigned)nblk(rows, kRankPerCta)), dim3(kThreads), 0, st,
-           (int)rows, (int)vocab, ids, p.sorted, p.head);
+           (int)rows, (int)vocab, ids, p.sorted, p.head, a.n_long);
     return cudaGetLastError();
   }
   const int per_block = (int)deal_rows(rows);
   const dim3 grid((unsigned)nblk(rows, per_block));
   int* base = p.head;
   launch(embed_count_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block, (int)vocab,
-         ids, p.counts);
+         ids, p.counts, a.n_long);
   launch(embed_deal_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block, (int)vocab,
          ids, (const int*)p.counts, p.dealt, base);
   const int bins = (int)((vocab - 1) / kBuckets + 1);
@@ -654,18 +796,13 @@ cudaError_t embed_scaled_fwd(int64_t rows, int64_t cols, int64_t vocab, int dt, 
   using bf16 = __nv_bfloat16;
   const int v = vec_width(cols, dt == DT_BF16 ? 2 : 4);
   if (dt == DT_BF16) {
-    switch (v) {
-      case 8: return fwd<bf16, 8>(rows, cols, vocab, scale, ids, table, y, st);
-      case 4: return fwd<bf16, 4>(rows, cols, vocab, scale, ids, table, y, st);
-      case 2: return fwd<bf16, 2>(rows, cols, vocab, scale, ids, table, y, st);
-      default: return fwd<bf16, 1>(rows, cols, vocab, scale, ids, table, y, st);
-    }
+    if (v == 8) return fwd<bf16, 8>(rows, cols, vocab, scale, ids, table, y, st);
+    if (v == 4) return fwd<bf16, 4>(rows, cols, vocab, scale, ids, table, y, st);
+    return fwd_odd<bf16>(rows, cols, vocab, scale, ids, table, y, st);
   }
-  switch (v) {
-    case 4: return fwd<float, 4>(rows, cols, vocab, scale, ids, table, y, st);
-    case 2: return fwd<float, 2>(rows, cols, vocab, scale, ids, table, y, st);
-    default: return fwd<float, 1>(rows, cols, vocab, scale, ids, table, y, st);
-  }
+  if (v == 4) return fwd<float, 4>(rows, cols, vocab, scale, ids, table, y, st);
+  if (v == 2) return fwd<float, 2>(rows, cols, vocab, scale, ids, table, y, st);
+  return fwd_odd<float>(rows, cols, vocab, scale, ids, table, y, st);
 }
 
 size_t embed_scaled_bwd_ws_bytes(int64_t rows, int64_t cols, int64_t vocab) {
@@ -686,6 +823,9 @@ cudaError_t embed_scaled_bwd(int64_t rows, int64_t cols, int64_t vocab, float sc
   a.dy = dy;
   a.d_table = d_table;
   a.partial = p.partial;
+  a.n_long = p.head + kBuckets + 1;
+  a.longs = p.longs;
+  a.max_longs = (int)p.max_longs;
   const int v = vec_width(cols, 4);
   if (rows <= kFewRows)
     return v == 4 ? accum_few<4>(a, st) : v == 2 ? accum_few<2>(a, st) : accum_few<1>(a, st);

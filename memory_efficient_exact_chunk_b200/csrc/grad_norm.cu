@@ -22,12 +22,14 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;
-// CTAs per SM of the summing pass and, where it joins the partial sums itself, of the clipping
-// (218 M elements: 16 / 32 take 410 us together, 8 / 8 442 us)
-constexpr int kSumBlocks = 16, kClipBlocks = 32;
-// pieces per SM above which the partial sums are joined by a launch of their own and the
-// clipping gives every piece a CTA (218 M elements: 395 us; 30 M: 74 us, 72 without)
-constexpr int kJoinPieces = 64;
+// CTAs per SM of the summing pass and of the clipping.  In place under the limit the clipping's
+// CTAs only read the sum and end, so they are kept few where the list is short (38 M elements:
+// 3 us at 8 per SM, 13 with a CTA per piece); a long list goes faster with a CTA per piece
+// (218 M elements: 248 us, 266 at 32 per SM).
+constexpr int kSumBlocks = 16, kClipBlocks = 32, kManyPieces = 128;
+// Up to this many pieces per SM every CTA of the clipping joins the partial sums itself; above,
+// a launch of its own does.
+constexpr int kJoinPieces = 8;
 // tensors of one launch: the small table where it is enough, as a launch copies its parameters
 constexpr int kSmallTable = 64, kLargeTable = 1024;
 
@@ -132,9 +134,10 @@ __global__ void __launch_bounds__(kThreads)
 sqsum_kernel(const __grid_constant__ Tensors<N> t, double* __restrict__ partial) {
   __shared__ double red[kThreads / 32];
   double s[4] = {};
-  Place at;
-  for (int64_t c = (int64_t)blockIdx.x * kPiece; c < t.units; c += (int64_t)gridDim.x * kPiece) {
-    at.find(t, c);
+  Place at, next;
+  next.find(t, (int64_t)blockIdx.x * kPiece);
+  for (int64_t c = (int64_t)blockIdx.x * kPiece; c < t.units;) {
+    at = next;
     float4 v[4];
     if (c + kPiece < at.to) {
       const float4* g = reinterpret_cast<const float4*>(t.src[at.i]) + (c - at.from) + threadIdx.x;
@@ -152,6 +155,8 @@ sqsum_kernel(const __grid_constant__ Tensors<N> t, double* __restrict__ partial)
         v[k] = load_unit(t.src[j] + x.at, x.have);
       }
     }
+    c += (int64_t)gridDim.x * kPiece;
+    if (c < t.units) next.find(t, c);      // while the loads are on their way
 #pragma unroll
     for (int k = 0; k < 4; ++k) s[k] += square(v[k]);
   }
@@ -163,13 +168,14 @@ sqsum_kernel(const __grid_constant__ Tensors<N> t, double* __restrict__ partial)
 __device__ __forceinline__ double join(int64_t n, const double* __restrict__ partial,
                                        double* red) {
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += kThreads) s += partial[i];
+  for (int64_t i = threadIdx.x; i < n; i += blockDim.x) s += partial[i];
   return block_sum(s, red);
 }
 
-__global__ void __launch_bounds__(kThreads)
+constexpr int kFinishThreads = 1024;
+__global__ void __launch_bounds__(kFinishThreads)
 sqsum_finish_kernel(int64_t n, const double* __restrict__ partial, double* __restrict__ sqsum) {
-  __shared__ double red[kThreads / 32];
+  __shared__ double red[kFinishThreads / 32];
   const double s = join(n, partial, red);
   if (threadIdx.x == 0) *sqsum = s;
 }
@@ -178,41 +184,40 @@ __device__ __forceinline__ float4 scaled(float4 v, float c) {
   return make_float4(v.x * c, v.y * c, v.z * c, v.w * c);
 }
 
-// The pieces are walked from the end: what was summed last is still in L2.
+// The pieces are taken from the end of the list: what was summed last is still in L2.
 template <int N>
 __global__ void __launch_bounds__(kThreads)
 clip_kernel(const __grid_constant__ Tensors<N> t, int64_t parts,
-            const double* __restrict__ partial, float max_norm, float* __restrict__ norm_out) {
+            const double* __restrict__ partial, float max_norm, bool in_place,
+            float* __restrict__ norm_out) {
   __shared__ double red[kThreads / 32];
   const double norm = sqrt(join(parts, partial, red));
   const float coef = clip_coef(norm, max_norm);
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
+  if (in_place && coef == 1.f) return;
   Place at;
-  const int64_t last = (t.units + kPiece - 1) / kPiece - 1;
-  for (int64_t p = last - blockIdx.x; p >= 0; p -= gridDim.x) {
+  for (int64_t p = (t.units + kPiece - 1) / kPiece - 1 - blockIdx.x; p >= 0; p -= gridDim.x) {
     const int64_t c = p * kPiece;
     at.find(t, c);
+    float4 v[4];
     if (c + kPiece < at.to) {
-      if (t.dst[at.i] == t.src[at.i] && coef == 1.f) continue;
       const int64_t o = c - at.from + threadIdx.x;
       const float4* g = reinterpret_cast<const float4*>(t.src[at.i]) + o;
       float4* d = reinterpret_cast<float4*>(t.dst[at.i]) + o;
-      float4 v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = g[k * kThreads];
 #pragma unroll
       for (int k = 0; k < 4; ++k) d[k * kThreads] = scaled(v[k], coef);
-    } else {
-      const int hi = at.behind(t, c);
+      continue;
+    }
+    const int hi = at.behind(t, c);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int64_t u = c + threadIdx.x + k * kThreads;
-        if (u >= t.units) continue;
-        const int j = tensor_of(t.end, at.i, hi, u);
-        if (t.dst[j] == t.src[j] && coef == 1.f) continue;
-        const Unit x(t.end, j, u);
-        store_unit(t.dst[j] + x.at, x.have, scaled(load_unit(t.src[j] + x.at, x.have), coef));
-      }
+    for (int k = 0; k < 4; ++k) {
+      const int64_t u = c + threadIdx.x + k * kThreads;
+      if (u >= t.units) continue;
+      const int j = tensor_of(t.end, at.i, hi, u);
+      const Unit x(t.end, j, u);
+      store_unit(t.dst[j] + x.at, x.have, scaled(load_unit(t.src[j] + x.at, x.have), coef));
     }
   }
 }
@@ -301,12 +306,15 @@ template <int N>
 void launch_clip(const GradTensors& g, int64_t parts, const double* partial, float max_norm,
                  float* norm_out, cudaStream_t st) {
   Tensors<N> t;
+  bool in_place = true;
+  for (int64_t i = 0; g.dst && i < g.n; ++i) in_place &= g.dst[i] == g.src[i] || g.numel[i] == 0;
   for (int64_t i = 0; i == 0 || i < g.n;) {     // one launch at least: it writes the norm
     i = imax(1, take(t, i, g));
     int64_t grid = pieces_of(t.units);
-    if (parts > 1) grid = imin(grid, (int64_t)sm_count() * kClipBlocks);
+    if (grid <= (int64_t)sm_count() * kManyPieces)
+      grid = imin(grid, (int64_t)sm_count() * kClipBlocks);
     launch(clip_kernel<N>, dim3((unsigned)grid), dim3(kThreads), 0, st, t, parts, partial,
-           max_norm, norm_out);
+           max_norm, in_place, norm_out);
     norm_out = nullptr;
   }
 }
@@ -330,7 +338,7 @@ int64_t sqsum_parts(const GradTensors& g, void* ws, cudaStream_t st) {
 }
 
 void sqsum_join(int64_t parts, void* ws, double* sqsum, cudaStream_t st) {
-  launch(sqsum_finish_kernel, dim3(1), dim3(kThreads), 0, st, parts,
+  launch(sqsum_finish_kernel, dim3(1), dim3(kFinishThreads), 0, st, parts,
          (const double*)partials(ws), sqsum);
 }
 

@@ -47,6 +47,8 @@ EMBED = [  # rows, cols, vocab, kind of ids
     (66000, 2, 1 << 22, "ends"), (17000, 24, 300, "sorted"), (16385, 24, 300, "reversed"),
     (256, 36, 1, "same"), (255, 130, 128256, "two"), (256, 4100, 30, "ends"), (257, 8, 4, "zipf"),
     (4096, 8, 5000, "zipf"), (4097, 8, 5000, "padded"), (300, 2, 200000, "uniform"),
+    (700, 1447, 50, "padded"), (8192, 12, 100, "zipf"), (9000, 264, 300, "zipf"),
+    (300000, 4, 1000, "zipf"), (2001, 666, 64, "uniform"), (5000, 2, 1, "same"),
 ]
 
 
