@@ -164,6 +164,7 @@ static_assert(kRankPerCta == kRankShare, "each of a row's threads takes one of t
 __global__ void __launch_bounds__(kThreads)
 embed_rank_kernel(int rows, int vocab, const int* __restrict__ ids, int4* __restrict__ sorted,
                   int* __restrict__ n_valid, int* __restrict__ n_long) {
+  release_next();
   __shared__ __align__(16) int key[kRankRows];
   const int rows4 = (rows + 3) / 4, padded = (rows + 15) / 16 * 16;
   for (int i = threadIdx.x; i < padded; i += kThreads) {
@@ -230,6 +231,7 @@ __global__ void __launch_bounds__(kDealThreads)
 embed_count_kernel(int rows, int per_block, int vocab, const int* __restrict__ ids,
                    int* __restrict__ counts, int* __restrict__ n_long) {
   __shared__ int hist[kBuckets];
+  release_next();
   if (blockIdx.x == 0 && threadIdx.x < 2) n_long[threadIdx.x] = 0;
   hist[threadIdx.x] = 0;
   __syncthreads();
@@ -276,6 +278,10 @@ embed_deal_kernel(int rows, int per_block, int vocab, const int* __restrict__ id
   int held[kHeld];
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) held[i] = r0 + 32 * i + lane < rows ? ids[r0 + 32 * i + lane] : -1;
+#pragma unroll
+  for (int w = 0; w < kDealWarps; ++w) hist[w][b] = 0;
+  release_next();
+  await_previous();
   int total = 0, before = 0;
 #pragma unroll 16
   for (int k = 0; k < (int)gridDim.x; ++k) {
@@ -283,8 +289,6 @@ embed_deal_kernel(int rows, int per_block, int vocab, const int* __restrict__ id
     total += c;
     if (k < (int)blockIdx.x) before += c;
   }
-#pragma unroll
-  for (int w = 0; w < kDealWarps; ++w) hist[w][b] = 0;
   const int start = block_exclusive_scan(total, red);
   if (blockIdx.x == 0) {
     base[b] = start;
@@ -341,8 +345,10 @@ embed_bucket_kernel(int vocab, int bins, int warps, const int* __restrict__ base
   int* start = sm + warps * bins;
   int* len = start + bins;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int b0 = base[blockIdx.x], n = base[blockIdx.x + 1] - b0;
   for (int i = threadIdx.x; i < warps * bins; i += kThreads) sm[i] = 0;
+  release_next();
+  await_previous();
+  const int b0 = base[blockIdx.x], n = base[blockIdx.x + 1] - b0;
   __syncthreads();
   const int per_warp = (n + warps * 32 - 1) / (warps * 32) * 32;
   const int i0 = b0 + wid * per_warp, i1 = min(b0 + n, i0 + per_warp);
@@ -487,12 +493,15 @@ __device__ __forceinline__ void put_row(const AccumArgs& a, int v, int64_t c, fl
 template <int V>
 __global__ void __launch_bounds__(kThreads)
 embed_accum_kernel(AccumArgs a) {
+  release_next();
   if ((int64_t)blockIdx.x >= a.acc_blocks) {
+    if (!a.ids) await_previous();       // by the ids, the clearing need not wait for the sort
     if (blockIdx.y == 0) clear_absent<V>(a, blockIdx.x - a.acc_blocks, gridDim.x - a.acc_blocks);
     return;
   }
   const int64_t c = ((int64_t)blockIdx.y * a.group + threadIdx.x % a.group) * V;
   const int g = threadIdx.x / a.group, groups = blockDim.x / a.group;
+  await_previous();
   const int n = *a.n_valid;
   const int64_t p0 = ((int64_t)blockIdx.x * groups + g) * a.window;
   const int p1 = (int)imin(n, p0 + a.window);
@@ -604,6 +613,7 @@ embed_join_kernel(AccumArgs a) {
   __shared__ float sums[kWarps][32 * V];
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int slabs = (int)((a.cols + 32 * V - 1) / (32 * V));
+  await_previous();
   // units [u0, u1) of the run that starts at `start`, eight of them in flight
   auto add = [&](int start, int u0, int u1, int64_t c, float (&sum)[V]) {
     const float* first = a.partial + 2 * (int64_t)(start / a.unit) * a.cols + c;
@@ -748,9 +758,9 @@ cudaError_t accum(AccumArgs a, cudaStream_t st) {
   a.acc_blocks = nblk(nblk(a.rows, a.window), groups);
   const int64_t clear = clear_blocks(a);
   a.unit = unit_rows(a.rows, a.cols);
-  launch(embed_accum_kernel<V>, dim3((unsigned)(a.acc_blocks + clear), (unsigned)slabs),
+  launch_next(embed_accum_kernel<V>, dim3((unsigned)(a.acc_blocks + clear), (unsigned)slabs),
          dim3(a.group * groups), 0, st, a);
-  launch(embed_join_kernel<V>, dim3(sm_count() * 4), dim3(kThreads), 0, st, a);
+  launch_next(embed_join_kernel<V>, dim3(sm_count() * 4), dim3(kThreads), 0, st, a);
   return cudaGetLastError();
 }
 
@@ -769,7 +779,7 @@ cudaError_t sort_by_id(int64_t rows, int64_t vocab, const int* ids, const Plan& 
   int* base = p.head;
   launch(embed_count_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block, (int)vocab,
          ids, p.counts, a.n_long);
-  launch(embed_deal_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block, (int)vocab,
+  launch_next(embed_deal_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block, (int)vocab,
          ids, (const int*)p.counts, p.dealt, base);
   const int bins = (int)((vocab - 1) / kBuckets + 1);
   int warps = kThreads / 32;      // as many histograms as 96 KB hold
@@ -780,7 +790,7 @@ cudaError_t sort_by_id(int64_t rows, int64_t vocab, const int* ids, const Plan& 
         embed_bucket_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
     if (e != cudaSuccess) return e;
   }
-  launch(embed_bucket_kernel, dim3(kBuckets), dim3(kThreads), smem, st, (int)vocab, bins, warps,
+  launch_next(embed_bucket_kernel, dim3(kBuckets), dim3(kThreads), smem, st, (int)vocab, bins, warps,
          (const int*)base, (const int2*)p.dealt, p.sorted,
          a.accumulate ? static_cast<unsigned char*>(nullptr) : p.present);
   a.n_valid = base + kBuckets;

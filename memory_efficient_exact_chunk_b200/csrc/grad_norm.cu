@@ -133,6 +133,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreads)
 sqsum_kernel(const __grid_constant__ Tensors<N> t, double* __restrict__ partial) {
   __shared__ double red[kThreads / 32];
+  release_next();
   double s[4] = {};
   Place at, next;
   next.find(t, (int64_t)blockIdx.x * kPiece);
@@ -176,6 +177,8 @@ constexpr int kFinishThreads = 1024;
 __global__ void __launch_bounds__(kFinishThreads)
 sqsum_finish_kernel(int64_t n, const double* __restrict__ partial, double* __restrict__ sqsum) {
   __shared__ double red[kFinishThreads / 32];
+  release_next();
+  await_previous();
   const double s = join(n, partial, red);
   if (threadIdx.x == 0) *sqsum = s;
 }
@@ -191,6 +194,8 @@ clip_kernel(const __grid_constant__ Tensors<N> t, int64_t parts,
             const double* __restrict__ partial, float max_norm, bool in_place,
             float* __restrict__ norm_out) {
   __shared__ double red[kThreads / 32];
+  release_next();
+  await_previous();
   const double norm = sqrt(join(parts, partial, red));
   const float coef = clip_coef(norm, max_norm);
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
@@ -304,7 +309,7 @@ int64_t launch_sqsum(const GradTensors& g, double* partial, cudaStream_t st) {
 
 template <int N>
 void launch_clip(const GradTensors& g, int64_t parts, const double* partial, float max_norm,
-                 float* norm_out, cudaStream_t st) {
+                 float* norm_out, bool after_sum, cudaStream_t st) {
   Tensors<N> t;
   bool in_place = true;
   for (int64_t i = 0; g.dst && i < g.n; ++i) in_place &= g.dst[i] == g.src[i] || g.numel[i] == 0;
@@ -313,8 +318,12 @@ void launch_clip(const GradTensors& g, int64_t parts, const double* partial, flo
     int64_t grid = pieces_of(t.units);
     if (grid <= (int64_t)sm_count() * kManyPieces)
       grid = imin(grid, (int64_t)sm_count() * kClipBlocks);
-    launch(clip_kernel<N>, dim3((unsigned)grid), dim3(kThreads), 0, st, t, parts, partial,
-           max_norm, in_place, norm_out);
+    if (after_sum)
+      launch_next(clip_kernel<N>, dim3((unsigned)grid), dim3(kThreads), 0, st, t, parts, partial,
+                  max_norm, in_place, norm_out);
+    else
+      launch(clip_kernel<N>, dim3((unsigned)grid), dim3(kThreads), 0, st, t, parts, partial,
+             max_norm, in_place, norm_out);
     norm_out = nullptr;
   }
 }
@@ -338,16 +347,16 @@ int64_t sqsum_parts(const GradTensors& g, void* ws, cudaStream_t st) {
 }
 
 void sqsum_join(int64_t parts, void* ws, double* sqsum, cudaStream_t st) {
-  launch(sqsum_finish_kernel, dim3(1), dim3(kFinishThreads), 0, st, parts,
+  launch_next(sqsum_finish_kernel, dim3(1), dim3(kFinishThreads), 0, st, parts,
          (const double*)partials(ws), sqsum);
 }
 
 void clip_parts(const GradTensors& g, int64_t parts, const double* partial, float max_norm,
-                float* norm_out, cudaStream_t st) {
+                float* norm_out, bool after_sum, cudaStream_t st) {
   if (g.n <= kSmallTable)
-    launch_clip<kSmallTable>(g, parts, partial, max_norm, norm_out, st);
+    launch_clip<kSmallTable>(g, parts, partial, max_norm, norm_out, after_sum, st);
   else
-    launch_clip<kLargeTable>(g, parts, partial, max_norm, norm_out, st);
+    launch_clip<kLargeTable>(g, parts, partial, max_norm, norm_out, after_sum, st);
 }
 
 }  // namespace
@@ -364,7 +373,7 @@ cudaError_t grad_sqsum(const GradTensors& g, double* sqsum, void* ws, cudaStream
 
 cudaError_t grad_clip(const GradTensors& g, const double* sqsum, float max_norm, float* norm_out,
                       cudaStream_t st) {
-  clip_parts(g, 1, sqsum, max_norm, norm_out, st);
+  clip_parts(g, 1, sqsum, max_norm, norm_out, false, st);
   return cudaGetLastError();
 }
 
@@ -384,11 +393,11 @@ cudaError_t grad_clip_norm(const GradTensors& g, float max_norm, float* norm_out
   }
   const int64_t parts = sqsum_parts(g, ws, st);
   if (pieces_of(units) <= (int64_t)sm_count() * kJoinPieces) {
-    clip_parts(g, parts, partials(ws), max_norm, norm_out, st);
+    clip_parts(g, parts, partials(ws), max_norm, norm_out, true, st);
   } else {
     double* sqsum = static_cast<double*>(ws);
     sqsum_join(parts, ws, sqsum, st);
-    clip_parts(g, 1, sqsum, max_norm, norm_out, st);
+    clip_parts(g, 1, sqsum, max_norm, norm_out, true, st);
   }
   return cudaGetLastError();
 }

@@ -268,6 +268,7 @@ qk_bwd_kernel(int rows, int hd, float inv_hd, int q_blocks, Heads<T> q, Heads<T>
               const float* __restrict__ cosb, const float* __restrict__ sinb, float eps,
               float* __restrict__ partial) {
   __shared__ float red[kWarps][256];
+  release_next();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, half = hd / 2;
   const bool is_k = (int)blockIdx.x >= q_blocks;
   const Heads<T>& t = is_k ? k : q;
@@ -385,6 +386,7 @@ qk_gain_kernel(int hd, int q_blocks, int blocks, const float* __restrict__ parti
   float* dst = blockIdx.y ? dk_g : dq_g;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float s = 0.f;
+  await_previous();
   if (c < hd) {
 #pragma unroll 8
     for (int b = b0 + wid; b < b1; b += 32) s += partial[(int64_t)b * hd + c];
@@ -520,7 +522,7 @@ cudaError_t qk_norm_rope_bwd(const QkNorm& a, float* dq_g, float* dk_g, float* p
     launch_type<__nv_bfloat16, true>(a, b, st);
   else
     launch_type<float, true>(a, b, st);
-  launch(qk_gain_kernel, dim3((unsigned)nblk(a.hd, 32), b.kb ? 2 : 1), dim3(1024), 0, st,
+  launch_next(qk_gain_kernel, dim3((unsigned)nblk(a.hd, 32), b.kb ? 2 : 1), dim3(1024), 0, st,
          (int)a.hd, b.qb, b.qb + b.kb, (const float*)partial, dq_g, dk_g);
   return cudaGetLastError();
 }

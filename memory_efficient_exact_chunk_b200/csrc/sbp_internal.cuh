@@ -46,6 +46,33 @@ inline void launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
   kernel<<<grid, block, smem, st>>>(std::forward<Args>(args)...);
 }
 
+// A launch whose grid may be set up, and its CTAs become resident, while the kernel before it on
+// the stream still runs (programmatic dependent launch): the kernel calls await_previous() before
+// it touches memory.  The kernel before it lets that happen early with release_next().
+template <typename... KArgs, typename... Args>
+inline void launch_next(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                        cudaStream_t st, Args&&... args) {
+  prof_count_launch();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  cudaLaunchKernelEx(&c, kernel, std::forward<Args>(args)...);
+}
+// waits until the kernels before this one on the stream have ended and their writes are visible
+__device__ __forceinline__ void await_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void release_next() {
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+
 enum Dt : int { DT_F32 = 0, DT_BF16 = 1 };
 
 // Message returned by sbp_last_error() on this thread (sbp_api.cu).

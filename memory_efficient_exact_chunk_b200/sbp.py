@@ -177,9 +177,17 @@ def chunk_bounds(seq_len: int, num_chunks: int):
 
 
 # ----------------------------------------------------------------------------- torch helpers
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    """torch, imported at the first use (the calls below are short: a global is cheaper than the
+    import statement)."""
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _ptr(t):
