@@ -404,7 +404,7 @@ embed_bucket_kernel(int vocab, int bins, int warps, const int* __restrict__ base
 // ---------------------------------------------------------------- accumulate
 // A run is cut into units of `unit` rows counted from its start.  A group of `group` threads
 // takes `window` consecutive sorted positions and adds every unit that begins there, all of its
-// rows in order, V columns per thread.  The unit of a run of one unit goes into the table; those
+// rows in order, four columns per thread (as 4 / V vectors a group apart).  The unit of a run of one unit goes into the table; those
 // of longer runs go to partial rows, which embed_join_kernel adds in order (the runs' starts are
 // left in two lists for it, in no particular order: the few of more than kLongUnits units from
 // the back).  In the list of
@@ -499,7 +499,10 @@ embed_accum_kernel(AccumArgs a) {
     if (blockIdx.y == 0) clear_absent<V>(a, blockIdx.x - a.acc_blocks, gridDim.x - a.acc_blocks);
     return;
   }
-  const int64_t c = ((int64_t)blockIdx.y * a.group + threadIdx.x % a.group) * V;
+  // the thread's columns: kV vectors, a group apart
+  constexpr int kV = 4 / V;
+  const int64_t c = ((int64_t)blockIdx.y * kV * a.group + threadIdx.x % a.group) * V;
+  const int64_t apart = (int64_t)a.group * V;
   const int g = threadIdx.x / a.group, groups = blockDim.x / a.group;
   await_previous();
   const int n = *a.n_valid;
@@ -513,44 +516,54 @@ embed_accum_kernel(AccumArgs a) {
   if (b >= p1) return;
   const int last = p1 - 1 - ((p1 - 1 - s1.y) & (a.unit - 1));
   const int e = min(last + a.unit, s1.y + s1.z);
-  float sum[V];
-  int4 run;             // of the unit in hand, and where the unit begins
+  float sum[kV][V];
+  int4 run = a.sorted[b];       // of the unit in hand, and where the unit begins
   int from = b;
   auto flush = [&]() {
-    if (run.z <= a.unit) {
-      put_row<V>(a, run.w, c, sum);
-      return;
+    const bool whole = run.z <= a.unit;
+    float* part = a.partial + (2 * (int64_t)(from / a.unit) + (from == run.y)) * a.cols;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+      if (c + v * apart >= a.cols) break;
+      if (whole)
+        put_row<V>(a, run.w, c + v * apart, sum[v]);
+      else
+        vstore<V>(part + c + v * apart, sum[v]);
     }
-    vstore<V>(a.partial + (2 * (int64_t)(from / a.unit) + (from == run.y)) * a.cols + c, sum);
-    if (from == run.y && c == 0) {
+    if (!whole && from == run.y && c == 0) {
       if (run.z <= a.unit * kLongUnits)
         a.longs[atomicAdd(a.n_long, 1)] = from;
       else
         a.longs[a.max_longs - 1 - atomicAdd(a.n_long + 1, 1)] = from;
     }
   };
-  // several rows in flight, whatever units they belong to
-  constexpr int kRows = V == 4 ? 4 : 8;
+  // four rows in flight, whatever units they belong to
+  constexpr int kRows = 4;
   for (int p = b; p < e; p += kRows) {
     int4 s[kRows];
-    float x[kRows][V];
+    float x[kRows][kV][V] = {};
 #pragma unroll
     for (int k = 0; k < kRows; ++k) s[k] = a.sorted[min(p + k, e - 1)];
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) vload<V>(a.dy + (int64_t)s[k].x * a.cols + c, x[k]);
+    for (int k = 0; k < kRows; ++k) {
+      const float* row = a.dy + (int64_t)s[k].x * a.cols + c;
+#pragma unroll
+      for (int v = 0; v < kV; ++v)
+        if (c + v * apart < a.cols) vload<V>(row + v * apart, x[k][v]);
+    }
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
       if (p + k >= e) break;
-      if (((p + k - s[k].y) & (a.unit - 1)) == 0) {
+      const bool begins = ((p + k - s[k].y) & (a.unit - 1)) == 0;
+      if (begins) {
         if (p + k > b) flush();
         run = s[k];
         from = p + k;
-#pragma unroll
-        for (int j = 0; j < V; ++j) sum[j] = x[k][j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) sum[j] += x[k][j];
       }
+#pragma unroll
+      for (int v = 0; v < kV; ++v)
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum[v][j] = begins ? x[k][v][j] : sum[v][j] + x[k][v][j];
     }
   }
   flush();
@@ -670,11 +683,14 @@ struct Plan {
   size_t bytes;
 };
 
+// slabs of columns that the groups of the accumulation take, 4 columns a thread
+int64_t slabs_of(int64_t cols) { return nblk(cols, 4 * kThreads); }
+
 // Rows of a unit: long units write few partial rows, short ones leave few sums in a row for a
 // group to wait for; a power of two that gives every SM sixteen groups' worth of full units
 // (6857 rows of 1312: 8, 13.9 us for the accumulation, 19.6 with 64; 64K rows of 4096: 64).
 int unit_rows(int64_t rows, int64_t cols) {
-  const int64_t slabs = nblk(cols, kThreads * vec_width(cols, 4));
+  const int64_t slabs = slabs_of(cols);
   int unit = kMinUnit;
   while (unit < kMaxUnit && rows * slabs >= (int64_t)sm_count() * 16 * 2 * unit) unit *= 2;
   return unit;
@@ -746,11 +762,11 @@ cudaError_t accum_few(AccumArgs a, cudaStream_t st) {
 
 template <int V>
 cudaError_t accum(AccumArgs a, cudaStream_t st) {
-  const int64_t nv = a.cols / V;
-  // the columns in equal slabs of at most 256 vectors; a group of whole warps takes one (of 8 or
-  // 16 threads where a row is shorter than a warp), a CTA as many groups as 256 threads hold
-  const int64_t slabs = nblk(nv, kThreads);
-  a.group = nv <= 8 ? 8 : nv <= 16 ? 16 : (int)nblk(nblk(nv, slabs), 32) * 32;
+  // the columns in equal slabs of at most 1024; a group of whole warps takes one (of 8 or 16
+  // threads where a slab is shorter than a warp), a CTA as many groups as 256 threads hold
+  const int64_t slabs = slabs_of(a.cols);
+  const int64_t threads = nblk(nblk(a.cols, slabs), 4);
+  a.group = threads <= 8 ? 8 : threads <= 16 ? 16 : (int)nblk(threads, 32) * 32;
   const int groups = kThreads / a.group;
   // positions per group: as many as leave every SM sixteen CTAs' worth of groups
   const int64_t fill = (int64_t)sm_count() * 16 * groups;
