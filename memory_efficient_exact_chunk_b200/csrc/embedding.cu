@@ -265,8 +265,7 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* red) {
 // number of valid rows
 __global__ void __launch_bounds__(kDealThreads)
 embed_deal_kernel(int rows, int per_block, int vocab, const int* __restrict__ ids,
-                  const int* __restrict__ counts, int2* __restrict__ dealt,
-                  int* __restrict__ base) {
+                  const int* counts, int2* __restrict__ dealt, int* __restrict__ base) {
   __shared__ int hist[kDealWarps][kBuckets];
   __shared__ int red[kDealWarps];
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -277,7 +276,8 @@ embed_deal_kernel(int rows, int per_block, int vocab, const int* __restrict__ id
   constexpr int kHeld = (int)kDealMinRows / kDealThreads;
   int held[kHeld];
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) held[i] = r0 + 32 * i + lane < rows ? ids[r0 + 32 * i + lane] : -1;
+  for (int i = 0; i < kHeld; ++i)
+    held[i] = r0 + 32 * i + lane < rows ? ids[r0 + 32 * i + lane] : -1;
 #pragma unroll
   for (int w = 0; w < kDealWarps; ++w) hist[w][b] = 0;
   release_next();
@@ -337,9 +337,8 @@ embed_deal_kernel(int rows, int per_block, int vocab, const int* __restrict__ id
 // memory: hist[warps][bins], start[bins], len[bins].  present[v] (where it is wanted) tells
 // whether id v occurs.
 __global__ void __launch_bounds__(kThreads)
-embed_bucket_kernel(int vocab, int bins, int warps, const int* __restrict__ base,
-                    const int2* __restrict__ dealt, int4* __restrict__ sorted,
-                    unsigned char* __restrict__ present) {
+embed_bucket_kernel(int vocab, int bins, int warps, const int* base, const int2* dealt,
+                    int4* __restrict__ sorted, unsigned char* __restrict__ present) {
   extern __shared__ int sm[];
   __shared__ int red[kThreads / 32];
   int* start = sm + warps * bins;
@@ -404,12 +403,12 @@ embed_bucket_kernel(int vocab, int bins, int warps, const int* __restrict__ base
 // ---------------------------------------------------------------- accumulate
 // A run is cut into units of `unit` rows counted from its start.  A group of `group` threads
 // takes `window` consecutive sorted positions and adds every unit that begins there, all of its
-// rows in order, four columns per thread (as 4 / V vectors a group apart).  The unit of a run of one unit goes into the table; those
-// of longer runs go to partial rows, which embed_join_kernel adds in order (the runs' starts are
-// left in two lists for it, in no particular order: the few of more than kLongUnits units from
-// the back).  In the list of
-// partial rows at most two units begin within `unit` positions: one that continues a run and one
-// that begins the next (a run longer than a unit leaves room for no third), which gives the slot
+// rows in order, four columns per thread (as 4 / V vectors a group apart).  The unit of a run of
+// one unit goes into the table; those of longer runs go to partial rows, which embed_join_kernel
+// adds in order (the runs' starts are left in two lists for it, in no particular order: the few
+// of more than kLongUnits units from the back).  Of the units that go to partial rows at most two
+// begin within `unit` positions: one that continues a run and one that begins the next (a run
+// longer than a unit leaves room for no third), which gives the slot
 // 2 (p / unit) + (p is its run's start).
 constexpr int kMaxUnit = 64, kMinUnit = 8, kLongUnits = 8;
 
@@ -642,7 +641,8 @@ embed_join_kernel(AccumArgs a) {
     }
   };
   const int64_t items = (int64_t)a.n_long[0] * slabs, heavy = (int64_t)a.n_long[1] * slabs;
-  for (int64_t i = (int64_t)blockIdx.x * kWarps + wid; i < items; i += (int64_t)gridDim.x * kWarps) {
+  for (int64_t i = (int64_t)blockIdx.x * kWarps + wid; i < items;
+       i += (int64_t)gridDim.x * kWarps) {
     const int64_t run = i / slabs, c = ((i - run * slabs) * 32 + lane) * V;
     const int4 s = a.sorted[a.longs[run]];
     if (c >= a.cols) continue;
@@ -739,8 +739,8 @@ cudaError_t fwd_odd(int64_t rows, int64_t cols, int64_t vocab, float scale, cons
                     const void* table, void* y, cudaStream_t st) {
   constexpr int64_t per = kFwdUnroll * kThreads * (8 / sizeof(T));
   launch(embed_scaled_fwd_odd_kernel<T>, dim3((unsigned)nblk(rows * cols, per)), dim3(kThreads),
-         0, st, rows * cols, Divisor((unsigned)cols), vocab, scale, ids, static_cast<const T*>(table),
-         static_cast<T*>(y));
+         0, st, rows * cols, Divisor((unsigned)cols), vocab, scale, ids,
+         static_cast<const T*>(table), static_cast<T*>(y));
   return cudaGetLastError();
 }
 
@@ -775,7 +775,7 @@ cudaError_t accum(AccumArgs a, cudaStream_t st) {
   const int64_t clear = clear_blocks(a);
   a.unit = unit_rows(a.rows, a.cols);
   launch_next(embed_accum_kernel<V>, dim3((unsigned)(a.acc_blocks + clear), (unsigned)slabs),
-         dim3(a.group * groups), 0, st, a);
+              dim3(a.group * groups), 0, st, a);
   launch_next(embed_join_kernel<V>, dim3(sm_count() * 4), dim3(kThreads), 0, st, a);
   return cudaGetLastError();
 }
@@ -795,8 +795,8 @@ cudaError_t sort_by_id(int64_t rows, int64_t vocab, const int* ids, const Plan& 
   int* base = p.head;
   launch(embed_count_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block, (int)vocab,
          ids, p.counts, a.n_long);
-  launch_next(embed_deal_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block, (int)vocab,
-         ids, (const int*)p.counts, p.dealt, base);
+  launch_next(embed_deal_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block,
+              (int)vocab, ids, (const int*)p.counts, p.dealt, base);
   const int bins = (int)((vocab - 1) / kBuckets + 1);
   int warps = kThreads / 32;      // as many histograms as 96 KB hold
   while (warps > 1 && (size_t)bins * (warps + 2) * 4 > 96 * 1024) warps /= 2;
@@ -806,9 +806,9 @@ cudaError_t sort_by_id(int64_t rows, int64_t vocab, const int* ids, const Plan& 
         embed_bucket_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
     if (e != cudaSuccess) return e;
   }
-  launch_next(embed_bucket_kernel, dim3(kBuckets), dim3(kThreads), smem, st, (int)vocab, bins, warps,
-         (const int*)base, (const int2*)p.dealt, p.sorted,
-         a.accumulate ? static_cast<unsigned char*>(nullptr) : p.present);
+  launch_next(embed_bucket_kernel, dim3(kBuckets), dim3(kThreads), smem, st, (int)vocab, bins,
+              warps, (const int*)base, (const int2*)p.dealt, p.sorted,
+              a.accumulate ? static_cast<unsigned char*>(nullptr) : p.present);
   a.n_valid = base + kBuckets;
   a.ids = nullptr;
   a.present = p.present;

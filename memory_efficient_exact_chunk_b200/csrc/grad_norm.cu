@@ -166,8 +166,7 @@ sqsum_kernel(const __grid_constant__ Tensors<N> t, double* __restrict__ partial)
 }
 
 // sum of the partial sums, the same bits in every CTA
-__device__ __forceinline__ double join(int64_t n, const double* __restrict__ partial,
-                                       double* red) {
+__device__ __forceinline__ double join(int64_t n, const double* partial, double* red) {
   double s = 0.0;
   for (int64_t i = threadIdx.x; i < n; i += blockDim.x) s += partial[i];
   return block_sum(s, red);
@@ -175,7 +174,7 @@ __device__ __forceinline__ double join(int64_t n, const double* __restrict__ par
 
 constexpr int kFinishThreads = 1024;
 __global__ void __launch_bounds__(kFinishThreads)
-sqsum_finish_kernel(int64_t n, const double* __restrict__ partial, double* __restrict__ sqsum) {
+sqsum_finish_kernel(int64_t n, const double* partial, double* __restrict__ sqsum) {
   __shared__ double red[kFinishThreads / 32];
   release_next();
   await_previous();
@@ -190,9 +189,8 @@ __device__ __forceinline__ float4 scaled(float4 v, float c) {
 // The pieces are taken from the end of the list: what was summed last is still in L2.
 template <int N>
 __global__ void __launch_bounds__(kThreads)
-clip_kernel(const __grid_constant__ Tensors<N> t, int64_t parts,
-            const double* __restrict__ partial, float max_norm, bool in_place,
-            float* __restrict__ norm_out) {
+clip_kernel(const __grid_constant__ Tensors<N> t, int64_t parts, const double* partial,
+            float max_norm, bool in_place, float* __restrict__ norm_out) {
   __shared__ double red[kThreads / 32];
   release_next();
   await_previous();

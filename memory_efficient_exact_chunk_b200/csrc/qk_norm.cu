@@ -379,7 +379,7 @@ qk_bwd_kernel(int rows, int hd, float inv_hd, int q_blocks, Heads<T> q, Heads<T>
 // dst[c] += sum of the blocks' partials, 32 columns of the queries' (y = 0) or the keys' (y = 1)
 // gain per CTA: each warp adds a 32nd of the partials, warp 0 the 32 sums in order.
 __global__ void __launch_bounds__(1024)
-qk_gain_kernel(int hd, int q_blocks, int blocks, const float* __restrict__ partial,
+qk_gain_kernel(int hd, int q_blocks, int blocks, const float* partial,
                float* __restrict__ dq_g, float* __restrict__ dk_g) {
   __shared__ float red[32][33];
   const int b0 = blockIdx.y ? q_blocks : 0, b1 = blockIdx.y ? blocks : q_blocks;

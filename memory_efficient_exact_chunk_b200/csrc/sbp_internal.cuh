@@ -48,7 +48,9 @@ inline void launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
 
 // A launch whose grid may be set up, and its CTAs become resident, while the kernel before it on
 // the stream still runs (programmatic dependent launch): the kernel calls await_previous() before
-// it touches memory.  The kernel before it lets that happen early with release_next().
+// it touches what that kernel writes, which it names by pointers without __restrict__ (loads by
+// a const __restrict__ pointer may be moved ahead of the wait).  The kernel before it lets that
+// happen early with release_next().
 template <typename... KArgs, typename... Args>
 inline void launch_next(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                         cudaStream_t st, Args&&... args) {

@@ -469,11 +469,14 @@ def _is(t, name, dtype, shape):
         raise ValueError(f"{name}: must be contiguous")
 
 
-def _step_ws(ws, need, dev):
-    if need == 0:
-        raise SbpError(1, "invalid sizes")
+def _step_ws(ws, need, dev, stream):
+    """ws, or a new workspace where it is too small.  (Sizes that the library refuses need 0
+    bytes; the call itself then says why.)"""
     if ws is None or ws.nbytes < need:
-        return workspace(need, f"cuda:{dev}")
+        ws = workspace(need, f"cuda:{dev}")
+        if stream is not None:           # allocated for the current stream, used on this one
+            ws.record_stream(stream)
+        return ws
     if not ws.is_contiguous() or ws.get_device() != dev:
         raise ValueError(f"the workspace must be a contiguous buffer on cuda:{dev}")
     return ws
@@ -511,7 +514,7 @@ def embedding_scaled_backward(ids, dy, scale, d_table, accumulate=True, ws=None,
     _is(d_table, "d_table", torch.float32, d_table.shape)
     _is(dy, "dy", torch.float32, (rows, cols) if dy.dim() == 2 else (*ids.shape, cols))
     dev, st = _on_device(stream, ids, dy, d_table)
-    ws = _step_ws(ws, embedding_scaled_backward_workspace_size(rows, cols, V), dev)
+    ws = _step_ws(ws, embedding_scaled_backward_workspace_size(rows, cols, V), dev, stream)
     _check(load().sbp_embedding_scaled_backward(rows, cols, V, scale, ids.data_ptr(),
                                                 dy.data_ptr(), d_table.data_ptr(),
                                                 1 if accumulate else 0, ws.data_ptr(), ws.nbytes,
@@ -606,7 +609,8 @@ def qk_norm_rope_backward(q, k, q_g, k_g, cos, sin, eps, dq_out, dk_out, dq, dk,
     dev, st = _on_device(stream, q, k, q_g, k_g, cos, sin, positions, dq_out, dk_out, dq, dk,
                          dq_g, dk_g)
     lib = load()
-    ws = _step_ws(ws, lib.sbp_qk_norm_rope_backward_workspace_size(args[0]), dev)
+    ws = _step_ws(ws, lib.sbp_qk_norm_rope_backward_workspace_size(args[0]), dev,
+                  stream)
     _check(lib.sbp_qk_norm_rope_backward(*args, dq_out.data_ptr(), lddqo, _addr(dk_out), lddko,
                                          dq.data_ptr(), lddq, _addr(dk), lddk, dq_g.data_ptr(),
                                          _addr(dk_g), ws.data_ptr(), ws.nbytes, st))
@@ -615,7 +619,8 @@ def qk_norm_rope_backward(q, k, q_g, k_g, cos, sin, eps, dq_out, dk_out, dq, dk,
 
 class GradList:
     """The gradients of a model in the form the norm and the clipping take: checked once, their
-    pointers and sizes in host arrays.  It holds the tensors."""
+    pointers and sizes in host arrays.  It holds the tensors.  No two may share memory (the
+    gradient of a tied weight belongs into the list once)."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
@@ -628,21 +633,45 @@ class GradList:
             if self.device < 0 or t.get_device() != self.device:
                 raise ValueError(f"gradient {i}: all gradients must be on one CUDA device")
         self.sizes = [t.numel() for t in self.tensors]
-        self.ptrs = (C.c_void_p * n)(*[t.data_ptr() for t in self.tensors])
+        ptrs = [t.data_ptr() for t in self.tensors]
+        self.ptrs = (C.c_void_p * n)(*ptrs)
         self.numel = (C.c_int64 * n)(*self.sizes)
+        # (start, end, index) of the non-empty ones by address
+        self.spans = sorted((p, p + 4 * m, i) for i, (p, m) in enumerate(zip(ptrs, self.sizes))
+                            if m)
+        for (_, end, i), (start, _, j) in zip(self.spans, self.spans[1:]):
+            if start < end:
+                raise ValueError(f"gradients {i} and {j} share memory")
 
     def __len__(self):
         return len(self.tensors)
+
+    def takes(self, out) -> bool:
+        """Whether the results may go to `out`: tensors of the same sizes, each either the
+        gradient itself or apart from every gradient."""
+        if out.sizes != self.sizes or out.device != self.device:
+            return False
+        a, b = self.spans, out.spans
+        if not a or a[-1][1] <= b[0][0] or b[-1][1] <= a[0][0]:
+            return True
+        i = 0
+        for start, end, k in b:
+            while i < len(a) and a[i][1] <= start:
+                i += 1
+            if i < len(a) and a[i][0] < end and a[i] != (start, end, k):
+                return False
+        return True
 
 
 def _grad_args(grads, out, stream, *scalars):
     if not isinstance(grads, GradList):
         grads = GradList(grads)
     into = None
-    if out is not None:
+    if out is not None and out is not grads:
         out = out if isinstance(out, GradList) else GradList(out)
-        if out.sizes != grads.sizes or out.device != grads.device:
-            raise ValueError("out must have the gradients' element counts and device")
+        if not grads.takes(out):
+            raise ValueError("out must have the gradients' sizes and device, and share memory "
+                             "with no other gradient than its own")
         into = out.ptrs
     dev, st = _on_device(stream, grads.tensors[0], *scalars)
     return grads, into, dev, st
@@ -657,7 +686,7 @@ def grad_sqsum(grads, sqsum, ws=None, stream=None):
     fp32 tensors).  Returns the workspace."""
     _is(sqsum, "sqsum", _torch().float64, (1,))
     grads, _, dev, st = _grad_args(grads, None, stream, sqsum)
-    ws = _step_ws(ws, grad_norm_workspace_size(len(grads)), dev)
+    ws = _step_ws(ws, grad_norm_workspace_size(len(grads)), dev, stream)
     _check(load().sbp_grad_sqsum(len(grads), grads.ptrs, grads.numel, sqsum.data_ptr(),
                                  ws.data_ptr(), ws.nbytes, st))
     return ws
@@ -679,7 +708,7 @@ def grad_clip_norm(grads, max_norm, norm_out, out=None, ws=None, stream=None):
     or into `out`).  Returns the workspace."""
     _is(norm_out, "norm_out", _torch().float32, (1,))
     grads, into, dev, st = _grad_args(grads, out, stream, norm_out)
-    ws = _step_ws(ws, grad_norm_workspace_size(len(grads)), dev)
+    ws = _step_ws(ws, grad_norm_workspace_size(len(grads)), dev, stream)
     _check(load().sbp_grad_clip_norm(len(grads), grads.ptrs, into, grads.numel, max_norm,
                                      norm_out.data_ptr(), ws.data_ptr(), ws.nbytes, st))
     return ws

@@ -414,6 +414,24 @@ def test_grad_clip_leaves_nonfinite_gradients_alone(bad, out):
         assert torch.equal(t.nan_to_num(nan=-5.0), k.nan_to_num(nan=-5.0))
 
 
+def test_grad_lists_that_share_memory_are_refused():
+    flat = torch.ones(1024, device="cuda")
+    a, b, c = flat[:256], flat[256:512], flat[512:768]
+    for bad in ([a, a], [a, flat[252:300]], [flat, b]):
+        with pytest.raises(ValueError, match="share memory"):
+            sbp.GradList(bad)
+    norm = torch.zeros(1, device="cuda")
+    for out in ([b, a], [b, c], [flat[4:260], c], [a], [c, flat[768:1000]]):
+        with pytest.raises(ValueError, match="out must"):
+            sbp.grad_clip_norm([a, b], 1.0, norm, out=out)
+    assert (flat == 1).all()
+    for out in ([a, b], [a, c], [c, b], [c, flat[768:]]):     # its own, or elsewhere
+        flat.fill_(1.0)
+        sbp.grad_clip_norm([a, b], 1.0, norm, out=out)
+        assert all(torch.equal(t, torch.full_like(t, float(t[0]))) for t in out)
+        assert abs(float(out[0][0]) - 1 / (512 ** 0.5)) < 1e-6
+
+
 def test_grad_sqsum_of_shards_adds_up():
     """Two ranks' shares of the gradients: their sums of squares add, each clips its own."""
     g = gen(9)
@@ -431,6 +449,35 @@ def test_grad_sqsum_of_shards_adds_up():
     assert abs(float(n2) - float(norm)) <= 2 * E * float(norm)
     for x, y in zip(a + b, whole):
         close(x, y.double(), y.double().abs() * 4 * E)
+
+
+def test_sizes_the_library_refuses():
+    """The wrappers pass the library's own status on."""
+    f = torch.zeros(1, device="cuda")
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    for call in (lambda: sbp.embedding_scaled_forward(none, f.view(1, 1), 1.0, f[:0].view(0, 1)),
+                 lambda: sbp.embedding_scaled_backward(none, f[:0].view(0, 1), 1.0, f.view(1, 1))):
+        with pytest.raises(sbp.SbpError) as e:
+            call()
+        assert e.value.code == 1
+    table = f.expand((1 << 22) + 1).contiguous().view(-1, 1)
+    with pytest.raises(sbp.SbpError) as e:
+        sbp.embedding_scaled_backward(torch.zeros(1, dtype=torch.int32, device="cuda"),
+                                      f.view(1, 1), 1.0, table)
+    assert e.value.code == 2
+    q, g, t = (torch.zeros(2, 1, 3, device="cuda"), torch.zeros(3, device="cuda"),
+               torch.zeros(2, 1, device="cuda"))
+    with pytest.raises(sbp.SbpError) as e:
+        sbp.qk_norm_rope_forward(q, None, g, None, t, t, 1e-6, q, None)
+    assert e.value.code == 2
+    with pytest.raises(sbp.SbpError) as e:          # more positions than the tables hold
+        sbp.qk_norm_rope_forward(torch.zeros(3, 1, 2, device="cuda"), None, g[:2], None, t, t,
+                                 1e-6, torch.zeros(3, 1, 2, device="cuda"), None)
+    assert e.value.code == 1
+    with pytest.raises(sbp.SbpError) as e:          # a workspace that is not 256-byte aligned
+        sbp.grad_sqsum([f], torch.zeros(1, dtype=torch.float64, device="cuda"),
+                       ws=sbp.workspace(1 << 20)[1:])
+    assert e.value.code == 1
 
 
 # --------------------------------------------------------------- streams, capture, sharing
