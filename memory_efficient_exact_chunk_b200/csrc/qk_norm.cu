@@ -179,44 +179,54 @@ __device__ __forceinline__ void store(T* p, const Lanes<kLw, kL>& ln, const F2 (
   }
 }
 
-// Forward.  The heads of all rows are one list; a warp takes U x per neighbours of it, all of
-// their loads in flight together and held as they came until their turn.  U = 2 where the
-// neighbours always lie in one row (4096 rows of 32 + 8 heads of 128: 19.3 us, 25 with U = 1).
+// Forward.  U = 1: the heads of all rows are one list, of which a warp takes `per` neighbours.
+// U = 2: a warp takes up to 2 x per heads of one row, all of their loads in flight together and
+// held as they came until their turn (4096 rows of 32 + 8 heads of 128: 17.3 us, 25 with U = 1).
 // Gain and angle are multiplied once per row, so a pair of elements costs
 //   y1 = rs (a (g c) - b (g' s)),  y2 = rs (b (g' c) + a (g s)).
+// CTAs of four warps fill the SM's places sooner than those of eight (32768 rows: 115 us, 119).
+constexpr int kFwdThreads = 128, kFwdWarps = kFwdThreads / 32;
 template <typename T, int U, int kLw, Layout kL>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kFwdThreads, 6)
 qk_fwd_kernel(int rows, int hd, float inv_hd, unsigned q_warps, unsigned warps, Heads<T> q,
               Heads<T> k, RowMap map, const float* __restrict__ cosb,
               const float* __restrict__ sinb, float eps) {
   const int half = hd / 2;
-  unsigned item = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  unsigned item = blockIdx.x * kFwdWarps + (threadIdx.x >> 5);
   if (item >= warps) return;
   const bool is_k = item >= q_warps;
   const Heads<T>& t = is_k ? k : q;
   if (is_k) item -= q_warps;
   const Lanes<kLw, kL> ln(threadIdx.x & 31, half);
   // the lane's heads: h of row r, and with U = 2 also h + per of the same row
-  const unsigned first = item * (U * ln.per);
-  int r = first / (unsigned)t.n;
-  int h = first - (unsigned)r * t.n + ln.sub;
-  if (U == 1 && h >= t.n) {        // a division only where a row ends
-    const int more = (unsigned)h / (unsigned)t.n;
-    r += more;
-    h -= more * t.n;
-  }
-  const bool in = U > 1 || r < rows;     // (with U = 2 the items divide the list evenly)
-  const int step = ln.per * hd;
-  Eight<T> a[U] = {}, b[U] = {};
-  if (in) {
-    const T* x = t.x + r * t.ldx + h * hd;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      a[u] = load(x + u * step, ln);
-      b[u] = load(x + u * step + half, ln);
+  int r, h;
+  if constexpr (U == 1) {
+    const unsigned first = item * ln.per;
+    r = first / (unsigned)t.n;
+    h = first - (unsigned)r * t.n + ln.sub;
+    if (h >= t.n) {        // a division only where a row ends
+      const int more = (unsigned)h / (unsigned)t.n;
+      r += more;
+      h -= more * t.n;
     }
+  } else {
+    const unsigned row_items = (unsigned)(t.n + U * ln.per - 1) / (U * ln.per);
+    r = item / row_items;
+    h = (item - (unsigned)r * row_items) * (U * ln.per) + ln.sub;
   }
-  const int64_t p = in ? map.pos(r) : -1;
+  // heads of the lane: none behind the last row, one where the row has no second; places without
+  // a head load the row's last one instead of branching, and store nothing
+  const int have = r >= rows ? 0 : U == 1 || h + ln.per >= t.n ? (h < t.n) : U;
+  r = min(r, rows - 1);
+  const T* x = t.x + r * t.ldx;
+  Eight<T> a[U], b[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const T* xh = x + min(h + u * ln.per, t.n - 1) * hd;
+    a[u] = load(xh, ln);
+    b[u] = load(xh + half, ln);
+  }
+  const int64_t p = map.pos(r);
   const bool ok = p >= 0 && p < map.table_len;
   F2 gc[4], gs[4], hc[4], hs[4];       // g c, -g' s, g' c, g s
   if (ok) {
@@ -233,7 +243,8 @@ qk_fwd_kernel(int rows, int hd, float inv_hd, unsigned q_warps, unsigned warps, 
       hc[i] = hc[i] * c[i];
     }
   }
-  T* y = in ? t.y + (is_k ? map.k_row(r) : r) * t.ldy + h * hd : nullptr;
+  T* y = t.y + (is_k ? map.k_row(r) : r) * t.ldy + h * hd;
+  const int step = ln.per * hd;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     F2 fa[4], fb[4], s2 = f2(0.f);
@@ -242,6 +253,7 @@ qk_fwd_kernel(int rows, int hd, float inv_hd, unsigned q_warps, unsigned warps, 
 #pragma unroll
     for (int i = 0; i < 4; ++i) s2 = fma2(fa[i], fa[i], fma2(fb[i], fb[i], s2));
     const F2 rs = f2(rsqrtf(fmaf(lanes_sum<kLw>(total(s2)), inv_hd, eps)));
+    if (u >= have) continue;
     if (ok) {
       F2 y1[4], y2[4];
 #pragma unroll
@@ -251,7 +263,7 @@ qk_fwd_kernel(int rows, int hd, float inv_hd, unsigned q_warps, unsigned warps, 
       }
       store(y + u * step, ln, y1);
       store(y + u * step + half, ln, y2);
-    } else if (in) {
+    } else {
       const F2 zero[4] = {};
       store(y + u * step, ln, zero);
       store(y + u * step + half, ln, zero);
@@ -450,22 +462,21 @@ struct Backward {
   float* partial;
 };
 
-template <typename T, int U, int kLw, Layout kL>
-void launch_fwd_heads(const QkNorm& a, cudaStream_t st) {
-  constexpr int per = U * (32 >> kLw);
-  const int64_t qw = nblk(a.rows * a.q.n, per), kw = nblk(a.rows * a.k.n, per);
-  launch(qk_fwd_kernel<T, U, kLw, kL>, dim3((unsigned)nblk(qw + kw, kWarps)), dim3(kThreads), 0,
-         st, (int)a.rows, (int)a.hd, 1.f / a.hd, (unsigned)qw, (unsigned)(qw + kw),
-         heads_of<T>(a.q), heads_of<T>(a.k), map_of(a), a.cosb, a.sinb, a.eps);
-}
-
 template <typename T, int kLw, Layout kL>
 void launch_fwd(const QkNorm& a, const Backward&, cudaStream_t st) {
+  constexpr int per = 32 >> kLw;
+  auto go = [&](auto kernel, int64_t qw, int64_t kw) {
+    launch(kernel, dim3((unsigned)nblk(qw + kw, kFwdWarps)), dim3(kFwdThreads), 0, st,
+           (int)a.rows, (int)a.hd, 1.f / a.hd, (unsigned)qw, (unsigned)(qw + kw),
+           heads_of<T>(a.q), heads_of<T>(a.k), map_of(a), a.cosb, a.sinb, a.eps);
+  };
   if constexpr (kL == kWide) {
-    constexpr int two = 2 * (32 >> kLw);
-    if (a.q.n % two == 0 && a.k.n % two == 0) return launch_fwd_heads<T, 2, kLw, kL>(a, st);
+    // two heads per lane unless more than a fifth of the places would be empty
+    const int64_t qi = nblk(a.q.n, 2 * per), ki = nblk(a.k.n, 2 * per);
+    if (8 * per * (qi + ki) <= 5 * (a.q.n + a.k.n))
+      return go(qk_fwd_kernel<T, 2, kLw, kL>, a.rows * qi, a.rows * ki);
   }
-  launch_fwd_heads<T, 1, kLw, kL>(a, st);
+  go(qk_fwd_kernel<T, 1, kLw, kL>, nblk(a.rows * a.q.n, per), nblk(a.rows * a.k.n, per));
 }
 
 template <typename T, int kLw, Layout kL>
