@@ -202,9 +202,9 @@ def _stream(stream=None):
 
 def _dtype_code(t):
     torch = _torch()
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return SBP_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return SBP_F32
     raise TypeError(f"unsupported dtype {t.dtype}")
 
@@ -445,19 +445,18 @@ def embedding_backward(ids, dy2d, d_table, ws=None, stream=None):
 def _on_device(stream, *tensors):
     """The index of the one CUDA device of `tensors` (None entries are left out) and the raw
     stream.  The library launches on the current device: tensors and stream have to be its."""
-    torch = _torch()
     dev = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError("tensors must be on one CUDA device")
     if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
-    if dev != torch.cuda.current_device() or (stream is not None and stream.device.index != dev):
+    # the device and the current stream's handle as torch keeps them: torch.cuda's own calls make
+    # a Stream object (3 us)
+    own = _torch()._C
+    if dev != own._cuda_getDevice() or (stream is not None and stream.device.index != dev):
         raise ValueError(f"tensors on cuda:{dev}: the current device and the stream must be its")
-    if stream is not None:
-        return dev, stream.cuda_stream
-    # the current stream's handle, without the Stream object that current_stream() makes (3 us)
-    return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, own._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _is(t, name, dtype, shape):
@@ -469,16 +468,22 @@ def _is(t, name, dtype, shape):
         raise ValueError(f"{name}: must be contiguous")
 
 
-def _step_ws(ws, need, dev, stream):
-    """ws, or a new workspace where it is too small.  (Sizes that the library refuses need 0
-    bytes; the call itself then says why.)"""
-    if ws is None or ws.nbytes < need:
-        ws = workspace(need, f"cuda:{dev}")
-        if stream is not None:           # allocated for the current stream, used on this one
-            ws.record_stream(stream)
-        return ws
-    if not ws.is_contiguous() or ws.get_device() != dev:
-        raise ValueError(f"the workspace must be a contiguous buffer on cuda:{dev}")
+def _with_ws(ws, dev, stream, need, call):
+    """call(address, bytes) with ws, or with a new workspace of need() bytes where ws is None or
+    too small for the library; the workspace used.  (Sizes that the library refuses need 0 bytes;
+    the call itself then says why.)"""
+    if ws is not None:
+        if not ws.is_contiguous() or ws.get_device() != dev:
+            raise ValueError(f"the workspace must be a contiguous buffer on cuda:{dev}")
+        code = call(ws.data_ptr(), ws.nbytes)
+        if code == 0:
+            return ws
+        if code != 3:                    # SBP_ERR_WORKSPACE, before anything is queued
+            _check(code)
+    ws = workspace(need(), f"cuda:{dev}")
+    if stream is not None:               # allocated for the current stream, used on this one
+        ws.record_stream(stream)
+    _check(call(ws.data_ptr(), ws.nbytes))
     return ws
 
 
@@ -489,15 +494,18 @@ def _addr(t):
 def embedding_scaled_forward(ids, table, scale, y, stream=None):
     """y[r] = scale * table[ids[r]]; ids int32, any shape; ids outside [0, vocab) give zero rows
     (include/sbp_step.h)."""
-    V, cols = table.shape
+    shape = table.shape
+    V, cols = shape
     rows = ids.numel()
-    dt = _dtype_code(table)
+    dtype, dt = table.dtype, _dtype_code(table)
     _is(ids, "ids", _torch().int32, ids.shape)
-    _is(table, "table", table.dtype, table.shape)
-    _is(y, "y", table.dtype, (rows, cols) if y.dim() == 2 else (*ids.shape, cols))
+    _is(table, "table", dtype, shape)
+    _is(y, "y", dtype, (rows, cols) if y.dim() == 2 else (*ids.shape, cols))
     _, st = _on_device(stream, ids, table, y)
-    _check(load().sbp_embedding_scaled_forward(rows, cols, V, dt, scale, ids.data_ptr(),
-                                               table.data_ptr(), y.data_ptr(), st))
+    code = load().sbp_embedding_scaled_forward(rows, cols, V, dt, scale, ids.data_ptr(),
+                                               table.data_ptr(), y.data_ptr(), st)
+    if code:
+        _check(code)
 
 
 def embedding_scaled_backward_workspace_size(rows, cols, vocab) -> int:
@@ -508,18 +516,18 @@ def embedding_scaled_backward(ids, dy, scale, d_table, accumulate=True, ws=None,
     """d_table (+)= scale * the sum of dy's rows of each id, by sorted tokens; without
     `accumulate` the whole table is written.  Returns the workspace, to be passed again."""
     torch = _torch()
-    V, cols = d_table.shape
+    shape = d_table.shape
+    V, cols = shape
     rows = ids.numel()
     _is(ids, "ids", torch.int32, ids.shape)
-    _is(d_table, "d_table", torch.float32, d_table.shape)
+    _is(d_table, "d_table", torch.float32, shape)
     _is(dy, "dy", torch.float32, (rows, cols) if dy.dim() == 2 else (*ids.shape, cols))
     dev, st = _on_device(stream, ids, dy, d_table)
-    ws = _step_ws(ws, embedding_scaled_backward_workspace_size(rows, cols, V), dev, stream)
-    _check(load().sbp_embedding_scaled_backward(rows, cols, V, scale, ids.data_ptr(),
-                                                dy.data_ptr(), d_table.data_ptr(),
-                                                1 if accumulate else 0, ws.data_ptr(), ws.nbytes,
-                                                st))
-    return ws
+    fn = load().sbp_embedding_scaled_backward
+    return _with_ws(ws, dev, stream,
+                    lambda: embedding_scaled_backward_workspace_size(rows, cols, V),
+                    lambda p, n: fn(rows, cols, V, scale, ids.data_ptr(), dy.data_ptr(),
+                                    d_table.data_ptr(), 1 if accumulate else 0, p, n, st))
 
 
 def rope_table(n_positions, head_dim, theta, device="cuda", stream=None):
@@ -553,27 +561,30 @@ def _heads(t, name, dtype, shape):
 
 
 def _qk_call(q, k, q_g, k_g, cos, sin, eps, positions, seq_len):
-    """Checks of what both directions share; the configuration and the leading arguments."""
+    """Checks of what both directions share; the leading arguments of both calls."""
     torch = _torch()
-    dtype = q.dtype
-    rows, H, hd = q.shape
-    dt = _dtype_code(q)
-    ldq = _heads(q, "q", dtype, q.shape)
-    _is(q_g, "q_g", dtype, (hd,))
-    Hkv = ldk = 0
-    if k is not None:
-        Hkv = k.shape[1]
-        ldk = _heads(k, "k", dtype, (rows, Hkv, hd))
-        _is(k_g, "k_g", dtype, (hd,))
-    table = (cos.shape[0], hd // 2)
+    dtype, dt, shape = q.dtype, _dtype_code(q), q.shape
+    rows, H, hd = shape
+    gain, table = (hd,), (cos.shape[0], hd // 2)
+    ldq = _heads(q, "q", dtype, shape)
+    _is(q_g, "q_g", dtype, gain)
     _is(cos, "cos", torch.float32, table)
     _is(sin, "sin", torch.float32, table)
+    pos = None
     if positions is not None:
         _is(positions, "positions", torch.int32, (rows,))
-    cfg = QkCfg(rows, H, Hkv, hd, rows if seq_len is None else seq_len, table[0], eps, dt)
-    return cfg, (C.byref(cfg), q.data_ptr(), ldq, _addr(k), ldk, q_g.data_ptr(),
-                 None if k is None else k_g.data_ptr(), _addr(positions), cos.data_ptr(),
-                 sin.data_ptr())
+        pos = positions.data_ptr()
+    seq = rows if seq_len is None else seq_len
+    if k is None:
+        cfg = QkCfg(rows, H, 0, hd, seq, table[0], eps, dt)
+        return (C.byref(cfg), q.data_ptr(), ldq, None, 0, q_g.data_ptr(), None, pos,
+                cos.data_ptr(), sin.data_ptr())
+    Hkv = k.shape[1]
+    ldk = _heads(k, "k", dtype, (rows, Hkv, hd))
+    _is(k_g, "k_g", dtype, gain)
+    cfg = QkCfg(rows, H, Hkv, hd, seq, table[0], eps, dt)
+    return (C.byref(cfg), q.data_ptr(), ldq, k.data_ptr(), ldk, q_g.data_ptr(), k_g.data_ptr(), pos,
+            cos.data_ptr(), sin.data_ptr())
 
 
 def qk_norm_rope_forward(q, k, q_g, k_g, cos, sin, eps, q_out, k_out, positions=None,
@@ -581,14 +592,16 @@ def qk_norm_rope_forward(q, k, q_g, k_g, cos, sin, eps, q_out, k_out, positions=
     """Per-head RMS norm with RoPE of q [rows, heads, head_dim] and k [rows, kv_heads, head_dim]
     (rows may be strided, k may be None) into q_out and k_out, which may be q and k
     (include/sbp_step.h).  The position of row r is positions[r], or r % seq_len (default: r)."""
-    _, args = _qk_call(q, k, q_g, k_g, cos, sin, eps, positions, seq_len)
+    args = _qk_call(q, k, q_g, k_g, cos, sin, eps, positions, seq_len)
     ldqo, ldko = _heads(q_out, "q_out", q.dtype, q.shape), 0
     if k is None:
         k_g = k_out = None
     else:
         ldko = _heads(k_out, "k_out", q.dtype, k.shape)
     _, st = _on_device(stream, q, k, q_g, k_g, cos, sin, positions, q_out, k_out)
-    _check(load().sbp_qk_norm_rope_forward(*args, q_out.data_ptr(), ldqo, _addr(k_out), ldko, st))
+    code = load().sbp_qk_norm_rope_forward(*args, q_out.data_ptr(), ldqo, _addr(k_out), ldko, st)
+    if code:
+        _check(code)
 
 
 def qk_norm_rope_backward(q, k, q_g, k_g, cos, sin, eps, dq_out, dk_out, dq, dk, dq_g, dk_g,
@@ -596,7 +609,7 @@ def qk_norm_rope_backward(q, k, q_g, k_g, cos, sin, eps, dq_out, dk_out, dq, dk,
     """Backward of qk_norm_rope_forward from its inputs: dq, dk overwritten (they may be dq_out,
     dk_out), dq_g, dk_g accumulated; all gradients fp32.  Returns the workspace."""
     f32 = _torch().float32
-    cfg, args = _qk_call(q, k, q_g, k_g, cos, sin, eps, positions, seq_len)
+    args = _qk_call(q, k, q_g, k_g, cos, sin, eps, positions, seq_len)
     gain = (q.shape[2],)
     lddqo, lddq = _heads(dq_out, "dq_out", f32, q.shape), _heads(dq, "dq", f32, q.shape)
     _is(dq_g, "dq_g", f32, gain)
@@ -609,12 +622,10 @@ def qk_norm_rope_backward(q, k, q_g, k_g, cos, sin, eps, dq_out, dk_out, dq, dk,
     dev, st = _on_device(stream, q, k, q_g, k_g, cos, sin, positions, dq_out, dk_out, dq, dk,
                          dq_g, dk_g)
     lib = load()
-    ws = _step_ws(ws, lib.sbp_qk_norm_rope_backward_workspace_size(args[0]), dev,
-                  stream)
-    _check(lib.sbp_qk_norm_rope_backward(*args, dq_out.data_ptr(), lddqo, _addr(dk_out), lddko,
-                                         dq.data_ptr(), lddq, _addr(dk), lddk, dq_g.data_ptr(),
-                                         _addr(dk_g), ws.data_ptr(), ws.nbytes, st))
-    return ws
+    return _with_ws(ws, dev, stream, lambda: lib.sbp_qk_norm_rope_backward_workspace_size(args[0]),
+                    lambda p, n: lib.sbp_qk_norm_rope_backward(
+                        *args, dq_out.data_ptr(), lddqo, _addr(dk_out), lddko, dq.data_ptr(),
+                        lddq, _addr(dk), lddk, dq_g.data_ptr(), _addr(dk_g), p, n, st))
 
 
 class GradList:
@@ -686,10 +697,9 @@ def grad_sqsum(grads, sqsum, ws=None, stream=None):
     fp32 tensors).  Returns the workspace."""
     _is(sqsum, "sqsum", _torch().float64, (1,))
     grads, _, dev, st = _grad_args(grads, None, stream, sqsum)
-    ws = _step_ws(ws, grad_norm_workspace_size(len(grads)), dev, stream)
-    _check(load().sbp_grad_sqsum(len(grads), grads.ptrs, grads.numel, sqsum.data_ptr(),
-                                 ws.data_ptr(), ws.nbytes, st))
-    return ws
+    n, fn = len(grads), load().sbp_grad_sqsum
+    return _with_ws(ws, dev, stream, lambda: grad_norm_workspace_size(n),
+                    lambda p, b: fn(n, grads.ptrs, grads.numel, sqsum.data_ptr(), p, b, st))
 
 
 def grad_clip(grads, sqsum, max_norm, norm_out=None, out=None, stream=None):
@@ -708,10 +718,10 @@ def grad_clip_norm(grads, max_norm, norm_out, out=None, ws=None, stream=None):
     or into `out`).  Returns the workspace."""
     _is(norm_out, "norm_out", _torch().float32, (1,))
     grads, into, dev, st = _grad_args(grads, out, stream, norm_out)
-    ws = _step_ws(ws, grad_norm_workspace_size(len(grads)), dev, stream)
-    _check(load().sbp_grad_clip_norm(len(grads), grads.ptrs, into, grads.numel, max_norm,
-                                     norm_out.data_ptr(), ws.data_ptr(), ws.nbytes, st))
-    return ws
+    n, fn = len(grads), load().sbp_grad_clip_norm
+    return _with_ws(ws, dev, stream, lambda: grad_norm_workspace_size(n),
+                    lambda p, b: fn(n, grads.ptrs, into, grads.numel, max_norm,
+                                    norm_out.data_ptr(), p, b, st))
 
 
 # ----------------------------------------------------------------------------- test hooks
