@@ -84,13 +84,13 @@ __device__ __forceinline__ double warp_sum64(double v) {
   return v;
 }
 
+// the block's sum in thread 0 (two levels of shuffles; red holds a value per warp)
 __device__ __forceinline__ double block_sum(double v, double* red) {
   v = warp_sum64(v);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  double s = 0.0;
-  for (int i = 0; i < (int)(blockDim.x >> 5); ++i) s += red[i];
-  return s;
+  if (threadIdx.x < 32) v = warp_sum64(threadIdx.x < blockDim.x / 32 ? red[threadIdx.x] : 0.0);
+  return v;
 }
 
 __device__ __forceinline__ double square(float v) { return (double)v * (double)v; }
@@ -165,7 +165,7 @@ sqsum_kernel(const __grid_constant__ Tensors<N> t, double* __restrict__ partial)
   if (threadIdx.x == 0) partial[blockIdx.x] = v;
 }
 
-// sum of the partial sums, the same bits in every CTA
+// sum of the partial sums in thread 0, the same bits in every CTA
 __device__ __forceinline__ double join(int64_t n, const double* partial, double* red) {
   double s = 0.0;
   for (int64_t i = threadIdx.x; i < n; i += blockDim.x) s += partial[i];
@@ -192,11 +192,17 @@ __global__ void __launch_bounds__(kThreads)
 clip_kernel(const __grid_constant__ Tensors<N> t, int64_t parts, const double* partial,
             float max_norm, bool in_place, float* __restrict__ norm_out) {
   __shared__ double red[kThreads / 32];
+  __shared__ float shared_coef;
   release_next();
   await_previous();
-  const double norm = sqrt(join(parts, partial, red));
-  const float coef = clip_coef(norm, max_norm);
-  if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
+  const double sum = join(parts, partial, red);
+  if (threadIdx.x == 0) {      // one thread's square root and division
+    const double norm = sqrt(sum);
+    shared_coef = clip_coef(norm, max_norm);
+    if (norm_out && blockIdx.x == 0) *norm_out = (float)norm;
+  }
+  __syncthreads();
+  const float coef = shared_coef;
   if (in_place && coef == 1.f) return;
   Place at;
   for (int64_t p = (t.units + kPiece - 1) / kPiece - 1 - blockIdx.x; p >= 0; p -= gridDim.x) {
@@ -234,6 +240,7 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads)
 clip_few_kernel(const __grid_constant__ Tensors<N> t, float max_norm,
                 float* __restrict__ norm_out) {
   __shared__ double red[kFewThreads / 32], sum;
+  __shared__ float shared_coef;
   __shared__ int64_t end[N];
   cg::cluster_group cluster = cg::this_cluster();
   for (int i = threadIdx.x; i < t.n; i += kFewThreads) end[i] = t.end[i];
@@ -259,13 +266,16 @@ clip_few_kernel(const __grid_constant__ Tensors<N> t, float max_norm,
   s = block_sum(s, red);
   if (threadIdx.x == 0) sum = s;
   cluster.sync();
-  s = 0.0;
+  if (threadIdx.x == 0) {
+    s = 0.0;
 #pragma unroll
-  for (int c = 0; c < kFewCtas; ++c) s += *cluster.map_shared_rank(&sum, c);
-  cluster.sync();           // no CTA ends while another reads its sum
-  const double norm = sqrt(s);
-  const float coef = clip_coef(norm, max_norm);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
+    for (int c = 0; c < kFewCtas; ++c) s += *cluster.map_shared_rank(&sum, c);
+    const double norm = sqrt(s);
+    shared_coef = clip_coef(norm, max_norm);
+    if (blockIdx.x == 0) *norm_out = (float)norm;
+  }
+  cluster.sync();           // the coefficient; and no CTA ends while another reads its sum
+  const float coef = shared_coef;
 #pragma unroll
   for (int k = 0; k < kFewUnits; ++k)
     if (have[k] > 0 && (dst[k] != src[k] || coef != 1.f))
