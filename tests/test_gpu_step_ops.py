@@ -480,6 +480,80 @@ def test_sizes_the_library_refuses():
     assert e.value.code == 1
 
 
+# ------------------------------------------------------- offsets past 32 bits, masked places
+def test_embedding_offsets_past_32_bits():
+    """A table of 2.3 G elements (9.2 GB): the last rows of it are used."""
+    vocab, cols = 140000, 16384
+    g = gen(41)
+    ids = torch.tensor([vocab - 1, 5, vocab - 2, vocab - 1, 0, 131073] * 50, dtype=torch.int32,
+                       device="cuda")
+    dy = torch.randn(len(ids), cols, generator=g, device="cuda")
+    table = torch.full((vocab, cols), float("nan"), device="cuda")
+    sbp.embedding_scaled_backward(ids, dy, 0.5, table, accumulate=False)
+    for v in ids.unique().tolist():
+        rows = dy[ids == v].double()
+        close(table[v], rows.sum(0) * 0.5, rows.abs().sum(0) * 0.5 * (len(rows) + 4) * E)
+    for v in (1, 100000, vocab - 3):
+        assert (table[v] == 0).all()
+    y = torch.empty_like(dy)
+    sbp.embedding_scaled_forward(ids, table, 2.0, y)
+    assert torch.equal(y, table[ids.long()] * 2.0)
+
+
+def test_qk_offsets_past_32_bits():
+    """Rows 8192 elements apart, 2.3 G elements from first to last."""
+    rows, H, hd, ld = 280000, 2, 64, 8192
+    x = torch.empty(rows, ld, dtype=torch.bfloat16, device="cuda")
+    q = x[:, 64:64 + H * hd].unflatten(1, (H, hd))
+    q.normal_(generator=gen(42))
+    gain = torch.ones(hd, dtype=torch.bfloat16, device="cuda")
+    cos, sin = qk_tables(1000, hd)
+    sbp.qk_norm_rope_forward(q, None, gain, None, cos, sin, 1e-6, q, None, seq_len=1000)
+    tail = q[-2500:].clone()
+    q.normal_(generator=gen(42))          # the inputs again
+    c, s, ok = qk_angles(None, 1000, 1000, cos, sin, rows)
+    want, mag = qk_reference(q[-2500:], gain, c[-2500:], s[-2500:], ok[-2500:], 1e-6)
+    close(tail, want, mag * (hd / 2 + 16) * E + want.abs() * 2.0 ** -8 * (1 + 2.0 ** -7))
+
+
+def test_clip_offsets_past_32_bits():
+    n = 2 ** 31 + 5
+    big, small = torch.full((n,), 1e-3, device="cuda"), torch.ones(3, device="cuda")
+    norm = torch.zeros(1, device="cuda")
+    v = float(np.float32(1e-3))
+    want = (n * v * v + 3) ** 0.5
+    sbp.grad_clip_norm([small, big], 1.0, norm)
+    assert abs(float(norm) - want) <= want * 2 * E
+    coef = 1.0 / (want + 1e-6)
+    for t, x in ((big[:4], v), (big[-6:], v), (big[2 ** 31 - 2:2 ** 31 + 2], v), (small, 1.0)):
+        close(t, torch.full_like(t, x, dtype=torch.float64) * coef, x * coef * 4 * E)
+    assert float(big.min()) == float(big.max())
+
+
+@pytest.mark.parametrize("hd,dt", [(128, "bf16"), (64, "f32"), (10, "bf16")])
+def test_rows_outside_the_tables_are_not_looked_at(hd, dt):
+    """NaN and infinities in rows whose position is outside stay where they are."""
+    g = gen(hd)
+    rows, H, Hkv = 41, 3, 1
+    q, k = qk_inputs(rows, H, Hkv, hd, dt, "fused", g)
+    gain = torch.ones(hd, dtype=DT[dt], device="cuda")
+    pos = torch.arange(rows, device="cuda", dtype=torch.int32)
+    pos[1::3] = -5
+    bad = pos < 0
+    cos, sin = qk_tables(rows, hd)
+    q[bad], k[bad] = float("nan"), float("inf")
+    qo, ko = torch.empty_like(q).contiguous(), torch.empty_like(k).contiguous()
+    sbp.qk_norm_rope_forward(q, k, gain, gain, cos, sin, 1e-6, qo, ko, positions=pos)
+    dqo, dko = qk_inputs(rows, H, Hkv, hd, "f32", "plain", g)
+    dqo[bad], dko[bad] = float("inf"), float("nan")
+    dq, dk, dg = torch.empty_like(dqo), torch.empty_like(dko), torch.zeros(2, hd, device="cuda")
+    sbp.qk_norm_rope_backward(q, k, gain, gain, cos, sin, 1e-6, dqo, dko, dq, dk, dg[0], dg[1],
+                              positions=pos)
+    for t in (qo, ko, dq, dk):
+        assert (t[bad] == 0).all() and torch.isfinite(t).all()
+    assert torch.isfinite(dg).all() and (dg != 0).any()
+
+
 # --------------------------------------------------------------- streams, capture, sharing
 def step_calls(g):
     """One call of each operator with its own buffers: (run, outputs, inputs)."""
