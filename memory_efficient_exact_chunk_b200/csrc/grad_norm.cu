@@ -33,6 +33,8 @@ constexpr int kJoinPieces = 8;
 // tensors of one launch: the small table where it is enough, as a launch copies its parameters
 constexpr int kSmallTable = 64, kLargeTable = 1024;
 
+constexpr int kIndex = 64;     // entries of a table's index
+
 template <int N>
 struct Tensors {
   int n;
@@ -41,6 +43,11 @@ struct Tensors {
                           // elements that its last unit lacks
   const float* src[N];
   float* dst[N];
+  // the tensor of every (1 << shift)-th unit: a search through 300 tensors starts between two of
+  // these and takes about three dependent loads, not nine (30 M elements: 61.4 us, 62.6 without;
+  // 2 M in 50 tensors: 10.0, 10.4)
+  int shift;
+  short first[kIndex + 1];
 };
 
 // the tensor in [lo, n) that unit u belongs to, by the table of ends
@@ -118,7 +125,8 @@ struct Place {
   template <int N>
   __device__ __forceinline__ void find(const Tensors<N>& t, int64_t u) {
     if (u >= from && u < to) return;
-    i = tensor_of(t.end, 0, t.n, u);
+    const int k = (int)(u >> t.shift);
+    i = tensor_of(t.end, t.first[k], t.first[k + 1] + 1, u);
     from = i ? t.end[i - 1] >> 2 : 0;
     to = t.end[i] >> 2;
   }
@@ -299,6 +307,19 @@ int64_t take(Tensors<N>& t, int64_t i, const GradTensors& g) {
   return i;
 }
 
+// the index of a table of at least one unit (of none: zeros, which no kernel reads)
+template <int N>
+void index(Tensors<N>& t) {
+  t.shift = 0;
+  while (((t.units - 1) >> t.shift) >= kIndex) ++t.shift;
+  int i = 0;
+  for (int k = 0; k <= kIndex; ++k) {
+    const int64_t u = imin((int64_t)k << t.shift, t.units - 1);
+    while (i + 1 < t.n && (t.end[i] >> 2) <= u) ++i;
+    t.first[k] = (short)i;
+  }
+}
+
 int64_t pieces_of(int64_t units) { return imax(1, (units + kPiece - 1) / kPiece); }
 
 template <int N>
@@ -308,6 +329,7 @@ int64_t launch_sqsum(const GradTensors& g, double* partial, cudaStream_t st) {
   for (int64_t i = 0; i < g.n;) {
     i = take(t, i, g);
     if (t.n == 0) break;
+    index(t);
     const int64_t grid = imin(pieces_of(t.units), (int64_t)sm_count() * kSumBlocks);
     launch(sqsum_kernel<N>, dim3((unsigned)grid), dim3(kThreads), 0, st, t, partial + parts);
     parts += grid;
@@ -323,6 +345,7 @@ void launch_clip(const GradTensors& g, int64_t parts, const double* partial, flo
   for (int64_t i = 0; g.dst && i < g.n; ++i) in_place &= g.dst[i] == g.src[i] || g.numel[i] == 0;
   for (int64_t i = 0; i == 0 || i < g.n;) {     // one launch at least: it writes the norm
     i = imax(1, take(t, i, g));
+    index(t);
     int64_t grid = pieces_of(t.units);
     if (grid <= (int64_t)sm_count() * kManyPieces)
       grid = imin(grid, (int64_t)sm_count() * kClipBlocks);
