@@ -5,6 +5,8 @@
 //
 // Both are bound by HBM: the forward reads the used table rows and writes y, the backward reads
 // dy once and reads and writes (or only writes) the table rows.
+#include <type_traits>
+
 #include "sbp_internal.cuh"
 
 namespace sbp {
@@ -29,9 +31,9 @@ __device__ __forceinline__ void store_last(Vec<T, V>* p, const Vec<T, V>& x) {
     *p = x;
 }
 
-// widest vector (elements) with which a row of cols elements of es bytes stays aligned
-int vec_width(int64_t cols, int es) {
-  int v = 16 / es;
+// widest vector of fp32 with which a row of cols elements stays aligned
+int vec_width(int64_t cols) {
+  int v = 4;
   while (cols % v) v /= 2;
   return v;
 }
@@ -89,62 +91,104 @@ embed_scaled_fwd_kernel(int64_t rows, Divisor by_nv, int64_t vocab, float scale,
   }
 }
 
-// Rows that no vector of 8 bytes fits (an odd number of elements, or 2 of bf16): y is still one
-// aligned array, so a thread writes 8 bytes of it with one access and gathers them one by one.
-template <typename T>
+// Rows that are no whole number of 16-byte vectors: kLanes threads take a row, or four vectors each
+// of it.  They write the vectors that are aligned in y; the elements of one lie in two aligned
+// vectors of the table, `by` elements behind the first one's start, and `by` is the same for the
+// whole row.  The elements before and behind y's vectors are moved one by one.  A warp's stores
+// begin at a 128-byte line where they can (60180 x 3209 in bf16: 92 us, 97 without; with element-
+// wise loads 147, with vectors of the whole list that shift by a variable 166: those two are bound
+// by the instructions they issue).
+template <typename T, int kBy>
+__device__ __forceinline__ uint4 shifted(uint4 lo, uint4 hi) {
+  const unsigned w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  constexpr int word = kBy * sizeof(T) / 4;
+  if constexpr (kBy * sizeof(T) % 4 != 0)
+    return make_uint4(__funnelshift_r(w[word], w[word + 1], 16),
+                      __funnelshift_r(w[word + 1], w[word + 2], 16),
+                      __funnelshift_r(w[word + 2], w[word + 3], 16),
+                      __funnelshift_r(w[word + 3], w[word + 4], 16));
+  else
+    return make_uint4(w[word], w[word + 1], w[word + 2], w[word + 3]);
+}
+
+// f(integral_constant n), for n in [kFrom, kTo)
+template <int kFrom, int kTo, typename F>
+__device__ __forceinline__ void with_constant(int n, F&& f) {
+  if constexpr (kFrom + 1 == kTo) {
+    f(std::integral_constant<int, kFrom>());
+  } else {
+    if (n == kFrom)
+      f(std::integral_constant<int, kFrom>());
+    else
+      with_constant<kFrom + 1, kTo>(n, f);
+  }
+}
+
+template <typename T, int kLanes>
 __global__ void __launch_bounds__(kThreads)
-embed_scaled_fwd_odd_kernel(int64_t n, Divisor by_cols, int64_t vocab, float scale,
+embed_scaled_fwd_odd_kernel(int64_t rows, int64_t cols, int64_t vocab, float scale, int lines,
                             const int* __restrict__ ids, const T* __restrict__ table,
                             T* __restrict__ y) {
-  constexpr int kV = 8 / sizeof(T);
-  const unsigned cols = by_cols.d;
-  const int64_t first = (int64_t)blockIdx.x * (kFwdUnroll * kThreads * kV);
-  const int64_t r0 = first / cols;
-  const unsigned c0 = (unsigned)(first - r0 * cols) + threadIdx.x * kV;
-  Vec<T, kV> x[kFwdUnroll];
-  bool ok[kFwdUnroll];
-#pragma unroll
-  for (int k = 0; k < kFwdUnroll; ++k) {
-    const int64_t i = first + (k * kThreads + threadIdx.x) * kV;
-    ok[k] = false;
-    if (i + kV > n) continue;
-    const unsigned o = c0 + k * kThreads * kV;
-    unsigned c;
-    const unsigned dr = by_cols.divide(o, c);
-    if (c + kV <= cols) {               // inside one row
-      const int64_t v = ids[r0 + dr];
-      ok[k] = v >= 0 && v < vocab;
-      const T* t = table + v * cols + c;
-      if (ok[k]) {
-#pragma unroll
-        for (int j = 0; j < kV; ++j) x[k].v[j] = t[j];
-      }
-    } else {                            // over a row's end
-      ok[k] = true;
-#pragma unroll
-      for (int j = 0; j < kV; ++j) {
-        unsigned cj;
-        const int64_t v = ids[r0 + by_cols.divide(o + j, cj)];
-        st_f(x[k].v, j, v >= 0 && v < vocab ? ld_f(table, v * cols + cj) : 0.f);
-      }
+  constexpr int kV = 16 / sizeof(T);
+  const int64_t r = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+  if (r >= rows) return;
+  const int lane = threadIdx.x % kLanes;
+  const int64_t v = ids[r];
+  const bool in = v >= 0 && v < vocab;
+  // columns [0, head) and [tail, cols) one by one
+  const int head = (int)imin(cols, -(r * cols) & (kV - 1));
+  const int vectors = (int)(cols - head) / kV, tail = head + vectors * kV;
+  // the first vector: with lines = 7 a warp's first one begins a line
+  const int j0 = (int)blockIdx.y * (kLanes * kFwdUnroll) + lane -
+                 (int)((r * cols + head) / kV & lines);
+  const T* src = table + (in ? v * cols : 0);
+  T* dst = y + r * cols;
+  if (blockIdx.y == 0) {
+    for (int i = lane; i < head + (int)cols - tail; i += kLanes) {
+      const int c = i < head ? i : tail + i - head;
+      st_f(dst, c, in ? scale * ld_f(src, c) : 0.f);
     }
   }
+  Vec<T, kV>* out = reinterpret_cast<Vec<T, kV>*>(dst + head);
+  if (!in) {
+    const Vec<T, kV> zero = {};
+#pragma unroll
+    for (int k = 0; k < kFwdUnroll; ++k) {
+      const int j = j0 + kLanes * k;
+      if (j >= 0 && j < vectors) store_last(out + j, zero);
+    }
+    return;
+  }
+  const int by = (int)((v * cols + head) & (kV - 1));
+  const uint4* t = reinterpret_cast<const uint4*>(src + head - by);
+  // the last vector of the table's last row may have its second half behind the table's end
+  const bool ends = by != 0 && v * cols + head - by + (int64_t)(vectors + 1) * kV > vocab * cols;
+  uint4 lo[kFwdUnroll], hi[kFwdUnroll];
 #pragma unroll
   for (int k = 0; k < kFwdUnroll; ++k) {
-    const int64_t i = first + (k * kThreads + threadIdx.x) * kV;
-    if (i >= n) break;
-    if (i + kV <= n) {
-#pragma unroll
-      for (int j = 0; j < kV; ++j) st_f(x[k].v, j, ok[k] ? scale * ld_f(x[k].v, j) : 0.f);
-      *reinterpret_cast<Vec<T, kV>*>(y + i) = x[k];
-    } else {                            // the last elements
-      for (int64_t e = i; e < n; ++e) {
-        const int64_t r = e / cols, v = ids[r];
-        const bool in = v >= 0 && v < vocab;
-        st_f(y, e, in ? scale * ld_f(table, v * cols + (e - r * cols)) : 0.f);
-      }
+    const int j = j0 + kLanes * k;
+    lo[k] = hi[k] = make_uint4(0, 0, 0, 0);
+    if (j < 0 || j >= vectors) continue;
+    lo[k] = t[j];
+    if (ends && j == vectors - 1) {
+      T* h = reinterpret_cast<T*>(&hi[k]);
+      for (int e = 0; e < by; ++e) h[e] = src[tail - by + e];
+    } else if (by != 0) {
+      hi[k] = t[j + 1];
     }
   }
+  with_constant<0, kV>(by, [&](auto n) {
+#pragma unroll
+    for (int k = 0; k < kFwdUnroll; ++k) {
+      const int j = j0 + kLanes * k;
+      if (j < 0 || j >= vectors) continue;
+      Vec<T, kV> x;
+      *reinterpret_cast<uint4*>(&x) = shifted<T, decltype(n)::value>(lo[k], hi[k]);
+#pragma unroll
+      for (int i = 0; i < kV; ++i) st_f(x.v, i, scale * ld_f(x.v, i));
+      store_last(out + j, x);
+    }
+  });
 }
 
 // ---------------------------------------------------------------- sort by id
@@ -223,6 +267,7 @@ embed_rank_kernel(int rows, int vocab, const int* __restrict__ ids, int4* __rest
 // places them; inside a warp equal keys are ranked by lane.
 constexpr int kBuckets = 512, kDealThreads = 512, kDealWarps = kDealThreads / 32;
 constexpr int64_t kDealMinRows = 2048, kDealMaxBlocks = 128;   // rows of a block at least; blocks
+constexpr int64_t kWideRows = 32768;      // above: buckets' CTAs of twice the threads
 
 __device__ __forceinline__ bool valid_id(int v, int vocab) { return v >= 0 && v < vocab; }
 
@@ -336,15 +381,15 @@ embed_deal_kernel(int rows, int per_block, int vocab, const int* __restrict__ id
 // One CTA per bucket: a counting sort by bin = id / kBuckets with `warps` histograms.  Shared
 // memory: hist[warps][bins], start[bins], len[bins].  present[v] (where it is wanted) tells
 // whether id v occurs.
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(2 * kThreads)
 embed_bucket_kernel(int vocab, int bins, int warps, const int* base, const int2* dealt,
                     int4* __restrict__ sorted, unsigned char* __restrict__ present) {
   extern __shared__ int sm[];
-  __shared__ int red[kThreads / 32];
+  __shared__ int red[2 * kThreads / 32];
   int* start = sm + warps * bins;
   int* len = start + bins;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  for (int i = threadIdx.x; i < warps * bins; i += kThreads) sm[i] = 0;
+  for (int i = threadIdx.x; i < warps * bins; i += blockDim.x) sm[i] = 0;
   release_next();
   await_previous();
   const int b0 = base[blockIdx.x], n = base[blockIdx.x + 1] - b0;
@@ -361,7 +406,7 @@ embed_bucket_kernel(int vocab, int bins, int warps, const int* base, const int2*
     }
   }
   __syncthreads();
-  const int per = (bins + kThreads - 1) / kThreads;
+  const int per = (bins + (int)blockDim.x - 1) / (int)blockDim.x;
   const int k0 = min(bins, (int)threadIdx.x * per), k1 = min(bins, k0 + per);
   int mine = 0;
   for (int k = k0; k < k1; ++k) {
@@ -762,10 +807,20 @@ cudaError_t fwd(int64_t rows, int64_t cols, int64_t vocab, float scale, const in
 template <typename T>
 cudaError_t fwd_odd(int64_t rows, int64_t cols, int64_t vocab, float scale, const int* ids,
                     const void* table, void* y, cudaStream_t st) {
-  constexpr int64_t per = kFwdUnroll * kThreads * (8 / sizeof(T));
-  launch(embed_scaled_fwd_odd_kernel<T>, dim3((unsigned)nblk(rows * cols, per)), dim3(kThreads),
-         0, st, rows * cols, Divisor((unsigned)cols), vocab, scale, ids,
-         static_cast<const T*>(table), static_cast<T*>(y));
+  const int64_t vectors = cols * (int64_t)sizeof(T) / 16;
+  auto go = [&](auto kernel, int lanes) {
+    const int64_t take = lanes * kFwdUnroll, parts = imax(1, nblk(vectors, take));
+    // from lines on where that needs no further part of the row
+    const int lines = lanes == 32 && vectors + 7 <= parts * take ? 7 : 0;
+    launch(kernel, dim3((unsigned)nblk(rows, kThreads / lanes), (unsigned)parts), dim3(kThreads),
+           0, st, rows, cols, vocab, scale, lines, ids, static_cast<const T*>(table),
+           static_cast<T*>(y));
+  };
+  // short rows by a quarter of a warp (60180 x 65: 6.7 us, 13.4 by a warp)
+  if (vectors <= 64)
+    go(embed_scaled_fwd_odd_kernel<T, 8>, 8);
+  else
+    go(embed_scaled_fwd_odd_kernel<T, 32>, 32);
   return cudaGetLastError();
 }
 
@@ -827,7 +882,10 @@ cudaError_t sort_by_id(int64_t rows, int64_t vocab, const int* ids, const Plan& 
   launch_next(embed_deal_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block,
               (int)vocab, ids, (const int*)p.counts, p.dealt, base);
   const int bins = (int)((vocab - 1) / kBuckets + 1);
-  int warps = kThreads / 32;      // as many histograms as 96 KB hold
+  // 512 threads where a frequent id may fill a bucket with thousands of rows (64K rows: 502 us in
+  // all, 505 with 256; 8570 rows: 26.5, 25.9)
+  const int threads = rows > kWideRows ? 2 * kThreads : kThreads;
+  int warps = threads / 32;      // as many histograms as 96 KB hold
   while (warps > 1 && (size_t)bins * (warps + 2) * 4 > 96 * 1024) warps /= 2;
   const size_t smem = sizeof(int) * (size_t)bins * (warps + 2);
   if (smem > 48 * 1024) {
@@ -835,7 +893,7 @@ cudaError_t sort_by_id(int64_t rows, int64_t vocab, const int* ids, const Plan& 
         embed_bucket_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
     if (e != cudaSuccess) return e;
   }
-  launch_next(embed_bucket_kernel, dim3(kBuckets), dim3(kThreads), smem, st, (int)vocab, bins,
+  launch_next(embed_bucket_kernel, dim3(kBuckets), dim3(threads), smem, st, (int)vocab, bins,
               warps, (const int*)base, (const int2*)p.dealt, p.sorted,
               a.accumulate ? static_cast<unsigned char*>(nullptr) : p.present);
   a.n_valid = base + kBuckets;
@@ -849,15 +907,11 @@ cudaError_t sort_by_id(int64_t rows, int64_t vocab, const int* ids, const Plan& 
 cudaError_t embed_scaled_fwd(int64_t rows, int64_t cols, int64_t vocab, int dt, float scale,
                              const int* ids, const void* table, void* y, cudaStream_t st) {
   using bf16 = __nv_bfloat16;
-  const int v = vec_width(cols, dt == DT_BF16 ? 2 : 4);
-  if (dt == DT_BF16) {
-    if (v == 8) return fwd<bf16, 8>(rows, cols, vocab, scale, ids, table, y, st);
-    if (v == 4) return fwd<bf16, 4>(rows, cols, vocab, scale, ids, table, y, st);
-    return fwd_odd<bf16>(rows, cols, vocab, scale, ids, table, y, st);
-  }
-  if (v == 4) return fwd<float, 4>(rows, cols, vocab, scale, ids, table, y, st);
-  if (v == 2) return fwd<float, 2>(rows, cols, vocab, scale, ids, table, y, st);
-  return fwd_odd<float>(rows, cols, vocab, scale, ids, table, y, st);
+  if (dt == DT_BF16)
+    return cols % 8 == 0 ? fwd<bf16, 8>(rows, cols, vocab, scale, ids, table, y, st)
+                         : fwd_odd<bf16>(rows, cols, vocab, scale, ids, table, y, st);
+  return cols % 4 == 0 ? fwd<float, 4>(rows, cols, vocab, scale, ids, table, y, st)
+                       : fwd_odd<float>(rows, cols, vocab, scale, ids, table, y, st);
 }
 
 size_t embed_scaled_bwd_ws_bytes(int64_t rows, int64_t cols, int64_t vocab) {
@@ -881,7 +935,7 @@ cudaError_t embed_scaled_bwd(int64_t rows, int64_t cols, int64_t vocab, float sc
   a.n_long = p.head + kBuckets + 1;
   a.longs = p.longs;
   a.max_longs = (int)p.max_longs;
-  const int v = vec_width(cols, 4);
+  const int v = vec_width(cols);
   if (rows <= kFewRows)
     return v == 4 ? accum_few<4>(a, st) : v == 2 ? accum_few<2>(a, st) : accum_few<1>(a, st);
   const cudaError_t e = sort_by_id(rows, vocab, ids, p, a, st);

@@ -90,6 +90,26 @@ def test_embedding_scaled_forward(rows, cols, vocab, kind, dt):
     untouched(buf, rows * cols)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [3, 67, 257, 259, 511, 518, 521, 1001, 1027, 1030, 1156, 4097])
+def test_embedding_scaled_forward_off_the_16_byte_grid(cols, dt):
+    """Rows at every offset, the table's last elements among them; what lies around the table is
+    not used, and a row of padding is +0 under a negative scale."""
+    g = gen(cols)
+    vocab, rows = 9, 75
+    buf, table = guarded(vocab, cols, dtype=DT[dt], fill=float("nan"))
+    table.copy_(torch.randn(vocab, cols, generator=g, device="cuda"))
+    ids = torch.arange(rows, device="cuda", dtype=torch.int32) * 7 % (vocab + 1)
+    ids[::5] = vocab - 1
+    out, y = guarded(rows, cols, dtype=DT[dt])
+    sbp.embedding_scaled_forward(ids, table, -1.7, y)
+    ok = ids < vocab
+    want = (table[torch.where(ok, ids, 0).long()].float() * float(np.float32(-1.7))).to(DT[dt])
+    assert torch.equal(y[ok], want[ok])
+    assert (y[~ok].float().view(torch.int32) == 0).all()
+    untouched(out, rows * cols)
+
+
 def grad_reference(ids, dy, scale, vocab, base):
     """d_table, the sum of the terms' magnitudes and the number of rows of each id, in fp64."""
     ok = (ids >= 0) & (ids < vocab)
