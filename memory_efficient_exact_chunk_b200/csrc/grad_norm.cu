@@ -130,10 +130,15 @@ struct Place {
     from = i ? t.end[i - 1] >> 2 : 0;
     to = t.end[i] >> 2;
   }
-  // behind the tensors that a unit of the piece at c can be in: mostly this one and the next
+  // behind the tensors that a unit of the piece at c can be in: mostly this one and the next; a
+  // short range keeps the units' own searches short (1 M elements in 200 tensors: 8.4 us, 10.4
+  // with a search to the list's end)
   template <int N>
   __device__ __forceinline__ int behind(const Tensors<N>& t, int64_t c) const {
-    return i + 1 < t.n && (t.end[i + 1] >> 2) >= c + kPiece ? i + 2 : t.n;
+    if (i + 1 < t.n && (t.end[i + 1] >> 2) >= c + kPiece) return i + 2;
+    const int64_t u = imin(c + kPiece, t.units) - 1;
+    const int k = (int)(u >> t.shift);
+    return tensor_of(t.end, max(i, t.first[k]), t.first[k + 1] + 1, u) + 1;
   }
 };
 
