@@ -233,14 +233,22 @@ clip_kernel(const __grid_constant__ Tensors<N> t, int64_t parts, const double* p
       continue;
     }
     const int hi = at.behind(t, c);
+    float* d[4];
+    int have[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int64_t u = c + threadIdx.x + k * kThreads;
+      have[k] = 0;
       if (u >= t.units) continue;
       const int j = tensor_of(t.end, at.i, hi, u);
       const Unit x(t.end, j, u);
-      store_unit(t.dst[j] + x.at, x.have, scaled(load_unit(t.src[j] + x.at, x.have), coef));
+      d[k] = t.dst[j] + x.at;
+      have[k] = x.have;
+      v[k] = load_unit(t.src[j] + x.at, x.have);
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (have[k] > 0) store_unit(d[k], have[k], scaled(v[k], coef));
   }
 }
 
