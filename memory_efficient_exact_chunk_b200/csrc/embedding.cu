@@ -763,12 +763,13 @@ struct Plan {
 int64_t slabs_of(int64_t cols) { return nblk(cols, 4 * kThreads); }
 
 // Rows of a unit: long units write few partial rows, short ones leave few sums in a row for a
-// group to wait for; a power of two that gives every SM sixteen groups' worth of full units
-// (6857 rows of 1312: 8, 13.9 us for the accumulation, 19.6 with 64; 64K rows of 4096: 64).
+// group to wait for; a power of two that gives every SM eight groups' worth of full units
+// (11132 rows of 1112: 16, 30.8 us in all, 34 with 8; 12043 of 2568: 32, 45.6, 51.3 with 8; 64K of
+// 4096: 64).
 int unit_rows(int64_t rows, int64_t cols) {
   const int64_t slabs = slabs_of(cols);
   int unit = kMinUnit;
-  while (unit < kMaxUnit && rows * slabs >= (int64_t)sm_count() * 16 * 2 * unit) unit *= 2;
+  while (unit < kMaxUnit && rows * slabs >= (int64_t)sm_count() * 8 * unit) unit *= 2;
   return unit;
 }
 
@@ -858,9 +859,10 @@ cudaError_t accum(AccumArgs a, cudaStream_t st) {
   const int64_t threads = nblk(nblk(a.cols, slabs), 4);
   a.group = threads <= 8 ? 8 : threads <= 16 ? 16 : (int)nblk(threads, 32) * 32;
   const int groups = kThreads / a.group;
-  // positions per group: as many as leave every SM sixteen CTAs' worth of groups
-  const int64_t fill = (int64_t)sm_count() * 16 * groups;
-  a.window = (int)imax(1, imin(32, a.rows * slabs / fill));
+  // positions per group: four at least, which are in flight together (4058 rows of 280: 13.4 us
+  // in all, 15.6 with one), and as many as leave every SM twelve CTAs' worth of groups
+  const int64_t fill = (int64_t)sm_count() * 12 * groups;
+  a.window = (int)imax(4, imin(64, a.rows * slabs / fill));
   a.acc_blocks = nblk(nblk(a.rows, a.window), groups);
   const int64_t clear = clear_blocks(a);
   a.unit = unit_rows(a.rows, a.cols);
@@ -868,7 +870,9 @@ cudaError_t accum(AccumArgs a, cudaStream_t st) {
               dim3(a.group * groups), sizeof(int4) * (groups * a.window + a.unit), st, a);
   // not set up early: its CTAs would hold the places of accumulating ones (11132 rows of 1112:
   // 33.9 us in all, 37.5 with them; 64K of 4096: 501, 502)
-  launch(embed_join_kernel<V>, dim3(sm_count() * 4), dim3(kThreads), 0, st, a);
+  // two columns a lane: twice the parts of a frequent id's run, and eight loads of it in flight
+  // (48890 rows of 440: 49.2 us in all, 55.0 with four; rare ids, 12043 rows of 2568: 51.4, 49.8)
+  launch(embed_join_kernel<V < 2 ? V : 2>, dim3(sm_count() * 4), dim3(kThreads), 0, st, a);
   return cudaGetLastError();
 }
 
