@@ -211,10 +211,23 @@ embed_rank_kernel(int rows, int vocab, const int* __restrict__ ids, int4* __rest
   release_next();
   __shared__ __align__(16) int key[kRankRows];
   const int rows4 = (rows + 3) / 4, padded = (rows + 15) / 16 * 16;
-  for (int i = threadIdx.x; i < padded; i += kThreads) {
-    const int v = i < rows ? ids[i] : -1;
-    key[i] = v < 0 || v >= vocab ? vocab : v;
+  int4* keys = reinterpret_cast<int4*>(key);
+  auto key_of = [&](int v) { return v < 0 || v >= vocab ? vocab : v; };
+  constexpr int kLoads = kRankRows / 4 / kThreads;
+  int4 v[kLoads];
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k) {
+    const int i = threadIdx.x + k * kThreads;
+    if (i < rows / 4) v[k] = reinterpret_cast<const int4*>(ids)[i];
   }
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k) {
+    const int i = threadIdx.x + k * kThreads;
+    if (i < rows / 4)
+      keys[i] = make_int4(key_of(v[k].x), key_of(v[k].y), key_of(v[k].z), key_of(v[k].w));
+  }
+  for (int i = rows / 4 * 4 + threadIdx.x; i < padded; i += kThreads)
+    key[i] = i < rows ? key_of(ids[i]) : vocab;
   __syncthreads();
   const int r0 = blockIdx.x * kRankPerCta, own = threadIdx.x / kRankShare;
   const int part = threadIdx.x % kRankShare;
