@@ -46,34 +46,69 @@ struct Heads {        // one of the two tensors (queries or keys)
   int64_t lddx;
 };
 
-// 1 << kLw lanes share a head (8 at head_dim 128; the next power of two where hd / 16 is none).
+// kN lanes share a head: a power of two (8 at head_dim 128; the next one where hd / 16 is none),
+// but 5 and 6 for heads of 80 and 96 in the vector layouts.  A warp takes 32 / kN heads, so two
+// of its lanes are left over there, where 8 lanes a head leave three or two of every eight
+// (backward of 16384 x (28 + 4) heads of 80 in bf16: 81 us, 99 with 8; of 96: 94, 104; heads of 48
+// gain nothing from 3 lanes: fp32 forward 45 us, 37 with 4).
 // A lane holds 8 elements of the first half of a head and the 8 that they are rotated with, so
 // the rotation needs no exchange.  Which 8:
 //   kWide    neighbours: one 16-byte access in bf16
 //   kSplit   two groups of 4, a group of lanes apart: the 16-byte accesses of neighbouring lanes
 //            to fp32 values lie side by side too (8 neighbours touch half of each sector twice)
-//   kScalar  every (1 << kLw)-th element, one by one: any even head_dim, any alignment
+//   kScalar  every kN-th element, one by one: any even head_dim, any alignment
 enum Layout { kWide, kSplit, kScalar };
-template <int kLw, Layout kL>
+template <int kN, Layout kL>
 struct Lanes {
-  static constexpr int per = 32 >> kLw;     // heads of a warp
-  int sub, l, half;                         // which of them, the lane in it
+  static constexpr int per = 32 / kN;       // heads of a warp
+  int sub, l, half;                         // which of them (per: a lane left over), the lane in it
   __device__ __forceinline__ Lanes(int lane, int half_)
-      : sub(lane >> kLw), l(lane & ((1 << kLw) - 1)), half(half_) {}
+      : sub(lane / kN), l(lane % kN), half(half_) {}
   // the lane's e-th element of either half
   __device__ __forceinline__ int at(int e) const {
     if constexpr (kL == kWide) return 8 * l + e;
-    if constexpr (kL == kSplit) return 4 * l + e + (e < 4 ? 0 : (4 << kLw) - 4);
-    return l + (e << kLw);
+    if constexpr (kL == kSplit) return 4 * l + e + (e < 4 ? 0 : 4 * kN - 4);
+    return l + e * kN;
   }
   __device__ __forceinline__ bool in(int e) const { return at(e) < half; }
-};
-template <int kLw>
-__device__ __forceinline__ float lanes_sum(float v) {
+  __device__ __forceinline__ bool left_over() const { return 32 % kN != 0 && sub == per; }
+  // the sum over the lanes of the head
+  __device__ __forceinline__ float sum(float v) const {
+    if constexpr ((kN & (kN - 1)) == 0) {
 #pragma unroll
-  for (int o = 1; o < (1 << kLw); o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
+      for (int o = 1; o < kN; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      return v;
+    }
+    // v becomes the sum of w lanes from the own one on; those of kN's bits are strung together
+    auto from = [&](float x, int k) {
+      const int j = l + k;
+      return __shfl_sync(0xffffffffu, x, sub * kN + (j < kN ? j : j - kN));
+    };
+    float s = 0.f;
+    int have = 0;
+#pragma unroll
+    for (int w = 1; w <= kN; w <<= 1) {
+      if (kN & w) {
+        s += have ? from(v, have) : v;
+        have += w;
+      }
+      if (2 * w <= kN) v += from(v, w);
+    }
+    return s;
+  }
+  // over the heads of the warp, for the lanes of the first
+  __device__ __forceinline__ float sum_heads(float v) const {
+    float s = v;
+    if constexpr ((kN & (kN - 1)) == 0) {
+#pragma unroll
+      for (int x = kN; x < 32; x <<= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+    } else {
+#pragma unroll
+      for (int h = 1; h < per; ++h) s += __shfl_down_sync(0xffffffffu, v, h * kN);
+    }
+    return s;
+  }
+};
 
 // Two fp32 values in a 64-bit register, for the two-wide fp32 instructions.  Both kernels were
 // bounded by the instructions that they issue as much as by HBM (two thirds of the slots): these,
@@ -142,8 +177,8 @@ template <typename T>
 struct alignas(16) Eight {
   Pack<T> lo, hi;
 };
-template <typename T, int kLw, Layout kL>
-__device__ __forceinline__ Eight<T> load(const T* p, const Lanes<kLw, kL>& ln) {
+template <typename T, int kN, Layout kL>
+__device__ __forceinline__ Eight<T> load(const T* p, const Lanes<kN, kL>& ln) {
   Eight<T> x = {};
   if constexpr (kL == kWide && sizeof(T) == 2) {
     if (ln.in(0)) *reinterpret_cast<uint4*>(&x) = *reinterpret_cast<const uint4*>(p + ln.at(0));
@@ -162,8 +197,8 @@ __device__ __forceinline__ void unpack(const Eight<T>& x, F2 (&f)[4]) {
   unpack(x.lo, f);
   unpack(x.hi, f + 2);
 }
-template <typename T, int kLw, Layout kL>
-__device__ __forceinline__ void store(T* p, const Lanes<kLw, kL>& ln, const F2 (&f)[4]) {
+template <typename T, int kN, Layout kL>
+__device__ __forceinline__ void store(T* p, const Lanes<kN, kL>& ln, const F2 (&f)[4]) {
   Eight<T> x;
   pack(f, x.lo);
   pack(f + 2, x.hi);
@@ -186,7 +221,7 @@ __device__ __forceinline__ void store(T* p, const Lanes<kLw, kL>& ln, const F2 (
 //   y1 = rs (a (g c) - b (g' s)),  y2 = rs (b (g' c) + a (g s)).
 // CTAs of four warps fill the SM's places sooner than those of eight (32768 rows: 115 us, 119).
 constexpr int kFwdThreads = 128, kFwdWarps = kFwdThreads / 32;
-template <typename T, int U, int kLw, Layout kL>
+template <typename T, int U, int kN, Layout kL>
 __global__ void __launch_bounds__(kFwdThreads, 6)
 qk_fwd_kernel(int rows, int hd, float inv_hd, unsigned q_warps, unsigned warps, Heads<T> q,
               Heads<T> k, RowMap map, const float* __restrict__ cosb,
@@ -197,7 +232,7 @@ qk_fwd_kernel(int rows, int hd, float inv_hd, unsigned q_warps, unsigned warps, 
   const bool is_k = item >= q_warps;
   const Heads<T>& t = is_k ? k : q;
   if (is_k) item -= q_warps;
-  const Lanes<kLw, kL> ln(threadIdx.x & 31, half);
+  const Lanes<kN, kL> ln(threadIdx.x & 31, half);
   // the lane's heads: h of row r, and with U = 2 also h + per of the same row
   int r, h;
   if constexpr (U == 1) {
@@ -216,7 +251,7 @@ qk_fwd_kernel(int rows, int hd, float inv_hd, unsigned q_warps, unsigned warps, 
   }
   // heads of the lane: none behind the last row, one where the row has no second; places without
   // a head load the row's last one instead of branching, and store nothing
-  const int have = r >= rows ? 0 : U == 1 || h + ln.per >= t.n ? (h < t.n) : U;
+  const int have = r >= rows || ln.left_over() ? 0 : U == 1 || h + ln.per >= t.n ? (h < t.n) : U;
   r = min(r, rows - 1);
   const T* x = t.x + r * t.ldx;
   Eight<T> a[U], b[U];
@@ -252,7 +287,7 @@ qk_fwd_kernel(int rows, int hd, float inv_hd, unsigned q_warps, unsigned warps, 
     unpack(b[u], fb);
 #pragma unroll
     for (int i = 0; i < 4; ++i) s2 = fma2(fa[i], fa[i], fma2(fb[i], fb[i], s2));
-    const F2 rs = f2(rsqrtf(fmaf(lanes_sum<kLw>(total(s2)), inv_hd, eps)));
+    const F2 rs = f2(rsqrtf(fmaf(ln.sum(total(s2)), inv_hd, eps)));
     if (u >= have) continue;
     if (ok) {
       F2 y1[4], y2[4];
@@ -274,7 +309,7 @@ qk_fwd_kernel(int rows, int hd, float inv_hd, unsigned q_warps, unsigned warps, 
 // Backward.  Blocks [0, q_blocks) take the queries, the others the keys.  Warps take `per`
 // neighbours of the list of heads in turn and keep the gain gradient of their elements in
 // registers; the block's sum goes to partial[block].
-template <typename T, int kLw, Layout kL>
+template <typename T, int kN, Layout kL>
 __global__ void __launch_bounds__(kThreads, 2)
 qk_bwd_kernel(int rows, int hd, float inv_hd, int q_blocks, Heads<T> q, Heads<T> k, RowMap map,
               const float* __restrict__ cosb, const float* __restrict__ sinb, float eps,
@@ -284,12 +319,13 @@ qk_bwd_kernel(int rows, int hd, float inv_hd, int q_blocks, Heads<T> q, Heads<T>
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, half = hd / 2;
   const bool is_k = (int)blockIdx.x >= q_blocks;
   const Heads<T>& t = is_k ? k : q;
-  const Lanes<kLw, kL> ln(lane, half);
+  const Lanes<kN, kL> ln(lane, half);
   const int warp = (is_k ? blockIdx.x - q_blocks : blockIdx.x) * kWarps + wid;
   const int stride = (is_k ? gridDim.x - q_blocks : q_blocks) * kWarps * ln.per;
   // the lane's first head, and the step to its next one, as row and head of the row
   const int first = warp * ln.per + ln.sub, step_r = stride / t.n, step_h = stride - step_r * t.n;
   int r = first / t.n, h = first - r * t.n;
+  if (ln.left_over()) r = rows;
   F2 ga[4], gb[4], da[4], db[4];
   unpack(load(t.g, ln), ga);
   unpack(load(t.g + half, ln), gb);
@@ -322,7 +358,7 @@ qk_bwd_kernel(int rows, int hd, float inv_hd, int q_blocks, Heads<T> q, Heads<T>
         }
       }
     }
-    const float rs = rsqrtf(fmaf(lanes_sum<kLw>(total(s2)), inv_hd, eps));
+    const float rs = rsqrtf(fmaf(ln.sum(total(s2)), inv_hd, eps));
     F2 dot2 = f2(0.f);
     if (ok) {
       const F2 r2 = f2(rs);
@@ -337,7 +373,7 @@ qk_bwd_kernel(int rows, int hd, float inv_hd, int q_blocks, Heads<T> q, Heads<T>
         dot2 = fma2(a[i], u[i], fma2(b[i], v[i], dot2));
       }
     }
-    const float dot = lanes_sum<kLw>(total(dot2)) * inv_hd;
+    const float dot = ln.sum(total(dot2)) * inv_hd;
     if (in) {
       float* dx = t.dx + r * t.lddx + h * hd;
       const F2 r2 = f2(rs), m = f2(-dot);
@@ -362,14 +398,9 @@ qk_bwd_kernel(int rows, int hd, float inv_hd, int q_blocks, Heads<T> q, Heads<T>
   // the warp's heads, then the block's warps in order
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float2 p = pair(da[i]), o = pair(db[i]);
-#pragma unroll
-    for (int x = 1 << kLw; x < 32; x <<= 1) {
-      p.x += __shfl_xor_sync(0xffffffffu, p.x, x);
-      p.y += __shfl_xor_sync(0xffffffffu, p.y, x);
-      o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
-      o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
-    }
+    const float2 da2 = pair(da[i]), db2 = pair(db[i]);
+    const float2 p = make_float2(ln.sum_heads(da2.x), ln.sum_heads(da2.y));
+    const float2 o = make_float2(ln.sum_heads(db2.x), ln.sum_heads(db2.y));
     if (ln.sub == 0 && ln.in(2 * i)) {
       red[wid][ln.at(2 * i)] = p.x;
       red[wid][ln.at(2 * i) + half] = o.x;
@@ -411,18 +442,19 @@ qk_gain_kernel(int hd, int q_blocks, int blocks, const float* partial,
   dst[c] += s;
 }
 
-// log2 of the lanes that share a head
-int lanes_log2(int64_t hd) {
-  int lw = 0;
-  while ((16 << lw) < hd) ++lw;
-  return lw;
+// lanes that share a head
+int lanes_of(int64_t hd, bool vec) {
+  if (vec && (hd == 80 || hd == 96)) return (int)hd / 16;
+  int n = 1;
+  while (16 * n < hd) n *= 2;
+  return n;
 }
 
 // blocks of the backward for the queries and the keys, in proportion to their heads; at most two
 // resident CTAs per SM, all in one wave
 int max_blocks() { return sm_count() * 2; }
-void bwd_blocks(const QkNorm& a, int& qb, int& kb) {
-  const int64_t cap = max_blocks(), per = kWarps * (32 >> lanes_log2(a.hd));
+void bwd_blocks(const QkNorm& a, int lanes, int& qb, int& kb) {
+  const int64_t cap = max_blocks(), per = kWarps * (32 / lanes);
   const int64_t qi = nblk(a.rows * a.q.n, per), ki = nblk(a.rows * a.k.n, per);
   if (qi + ki <= cap) {
     qb = (int)qi;
@@ -462,9 +494,9 @@ struct Backward {
   float* partial;
 };
 
-template <typename T, int kLw, Layout kL>
+template <typename T, int kN, Layout kL>
 void launch_fwd(const QkNorm& a, const Backward&, cudaStream_t st) {
-  constexpr int per = 32 >> kLw;
+  constexpr int per = 32 / kN;
   auto go = [&](auto kernel, int64_t qw, int64_t kw) {
     launch(kernel, dim3((unsigned)nblk(qw + kw, kFwdWarps)), dim3(kFwdThreads), 0, st,
            (int)a.rows, (int)a.hd, 1.f / a.hd, (unsigned)qw, (unsigned)(qw + kw),
@@ -474,33 +506,38 @@ void launch_fwd(const QkNorm& a, const Backward&, cudaStream_t st) {
     // two heads per lane unless more than a fifth of the places would be empty
     const int64_t qi = nblk(a.q.n, 2 * per), ki = nblk(a.k.n, 2 * per);
     if (8 * per * (qi + ki) <= 5 * (a.q.n + a.k.n))
-      return go(qk_fwd_kernel<T, 2, kLw, kL>, a.rows * qi, a.rows * ki);
+      return go(qk_fwd_kernel<T, 2, kN, kL>, a.rows * qi, a.rows * ki);
   }
-  go(qk_fwd_kernel<T, 1, kLw, kL>, nblk(a.rows * a.q.n, per), nblk(a.rows * a.k.n, per));
+  go(qk_fwd_kernel<T, 1, kN, kL>, nblk(a.rows * a.q.n, per), nblk(a.rows * a.k.n, per));
 }
 
-template <typename T, int kLw, Layout kL>
+template <typename T, int kN, Layout kL>
 void launch_bwd(const QkNorm& a, const Backward& b, cudaStream_t st) {
-  launch(qk_bwd_kernel<T, kLw, kL>, dim3(b.qb + b.kb), dim3(kThreads), 0, st, (int)a.rows,
+  launch(qk_bwd_kernel<T, kN, kL>, dim3(b.qb + b.kb), dim3(kThreads), 0, st, (int)a.rows,
          (int)a.hd, 1.f / a.hd, b.qb, heads_of<T>(a.q), heads_of<T>(a.k), map_of(a), a.cosb,
          a.sinb, a.eps, b.partial);
 }
 
 template <typename T, Layout kL, bool kBwd>
 void launch_width(const QkNorm& a, const Backward& b, cudaStream_t st) {
-  auto go = [&](auto lw) {
-    constexpr int kLw = decltype(lw)::value;
+  auto go = [&](auto lanes) {
+    constexpr int kN = decltype(lanes)::value;
     if constexpr (kBwd)
-      launch_bwd<T, kLw, kL>(a, b, st);
+      launch_bwd<T, kN, kL>(a, b, st);
     else
-      launch_fwd<T, kLw, kL>(a, b, st);
+      launch_fwd<T, kN, kL>(a, b, st);
   };
-  switch (lanes_log2(a.hd)) {
-    case 0: return go(std::integral_constant<int, 0>());
+  const int lanes = lanes_of(a.hd, kL != kScalar);
+  if constexpr (kL != kScalar) {
+    if (lanes == 5) return go(std::integral_constant<int, 5>());
+    if (lanes == 6) return go(std::integral_constant<int, 6>());
+  }
+  switch (lanes) {
     case 1: return go(std::integral_constant<int, 1>());
     case 2: return go(std::integral_constant<int, 2>());
-    case 3: return go(std::integral_constant<int, 3>());
-    default: return go(std::integral_constant<int, 4>());
+    case 4: return go(std::integral_constant<int, 4>());
+    case 8: return go(std::integral_constant<int, 8>());
+    default: return go(std::integral_constant<int, 16>());
   }
 }
 
@@ -527,7 +564,7 @@ size_t qk_norm_bwd_partial_floats(int64_t hd) { return (size_t)max_blocks() * hd
 cudaError_t qk_norm_rope_bwd(const QkNorm& a, float* dq_g, float* dk_g, float* partial,
                              cudaStream_t st) {
   Backward b;
-  bwd_blocks(a, b.qb, b.kb);
+  bwd_blocks(a, lanes_of(a.hd, vec_ok(a, true)), b.qb, b.kb);
   b.partial = partial;
   if (a.dt == DT_BF16)
     launch_type<__nv_bfloat16, true>(a, b, st);

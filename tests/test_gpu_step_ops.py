@@ -218,6 +218,10 @@ QK = [  # rows, heads, kv heads, head_dim, dtype, layout, positions
     (700, 1, 512, 16, "bf16", "plain", 700), (999, 1, 3, 8, "f32", "fused", "outside"),
     (1500, 5, 2, 24, "bf16", "plain", "any"), (333, 3, 1, 256, "bf16", "fused", 111),
     (2000, 7, 1, 102, "bf16", "fused", "any"), (600, 2, 2, 254, "f32", "plain", None),
+    (1, 1, 1, 80, "bf16", "plain", None), (515, 7, 3, 80, "bf16", "fused", "outside"),
+    (1003, 12, 12, 80, "f32", "plain", "any"), (3001, 28, 4, 80, "bf16", "plain", 3001),
+    (64, 32, 8, 96, "f32", "plain", 64), (2, 1, 11, 96, "bf16", "fused", "outside"),
+    (1777, 5, 1, 96, "bf16", "plain", "any"), (31, 6, 2, 80, "bf16", "odd", None),
 ]
 
 
