@@ -14,7 +14,7 @@ namespace sbp {
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 
 inline int64_t nblk(int64_t n, int64_t t) { return (n + t - 1) / t; }
 
@@ -219,10 +219,17 @@ __device__ __forceinline__ void store(T* p, const Lanes<kN, kL>& ln, const F2 (&
 // held as they came until their turn (4096 rows of 32 + 8 heads of 128: 17.3 us, 25 with U = 1).
 // Gain and angle are multiplied once per row, so a pair of elements costs
 //   y1 = rs (a (g c) - b (g' s)),  y2 = rs (b (g' c) + a (g s)).
-// CTAs of four warps fill the SM's places sooner than those of eight (32768 rows: 115 us, 119).
-constexpr int kFwdThreads = 128, kFwdWarps = kFwdThreads / 32;
+// Small CTAs fill the SM's places sooner, and as many warps as the registers of their loads leave
+// room for hide more of the latency (16384 x (28 + 4) heads of 128 in bf16: 28 warps per SM 50.4
+// us, 24 53.7; U = 1, heads of 80: 32 warps 42.0, 24 48.3; scalar bf16, heads of 102: 28 warps 88,
+// 32 97).
+constexpr int kFwdThreads = 64, kFwdWarps = kFwdThreads / 32;
+template <typename T, int U, Layout kL>
+constexpr int fwd_blocks() {
+  return U == 1 && (kL != kScalar || sizeof(T) == 4) ? 16 : 14;
+}
 template <typename T, int U, int kN, Layout kL>
-__global__ void __launch_bounds__(kFwdThreads, 6)
+__global__ void __launch_bounds__(kFwdThreads, (fwd_blocks<T, U, kL>()))
 qk_fwd_kernel(int rows, int hd, float inv_hd, unsigned q_warps, unsigned warps, Heads<T> q,
               Heads<T> k, RowMap map, const float* __restrict__ cosb,
               const float* __restrict__ sinb, float eps) {
@@ -308,9 +315,13 @@ qk_fwd_kernel(int rows, int hd, float inv_hd, unsigned q_warps, unsigned warps, 
 
 // Backward.  Blocks [0, q_blocks) take the queries, the others the keys.  Warps take `per`
 // neighbours of the list of heads in turn and keep the gain gradient of their elements in
-// registers; the block's sum goes to partial[block].
+// registers; the block's sum goes to partial[block].  One wave of CTAs: 20 warps per SM where the
+// registers of their loads leave room (16384 x (28 + 4) heads of 128: bf16 111 us, 115 with 16;
+// fp32 136, 125 with 16).
+constexpr int kBwdBlocks = 5;
+constexpr int bwd_blocks_per_sm(bool bf16, bool vec) { return bf16 && vec ? kBwdBlocks : 4; }
 template <typename T, int kN, Layout kL>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, bwd_blocks_per_sm(sizeof(T) == 2, kL != kScalar))
 qk_bwd_kernel(int rows, int hd, float inv_hd, int q_blocks, Heads<T> q, Heads<T> k, RowMap map,
               const float* __restrict__ cosb, const float* __restrict__ sinb, float eps,
               float* __restrict__ partial) {
@@ -450,21 +461,6 @@ int lanes_of(int64_t hd, bool vec) {
   return n;
 }
 
-// blocks of the backward for the queries and the keys, in proportion to their heads; at most two
-// resident CTAs per SM, all in one wave
-int max_blocks() { return sm_count() * 2; }
-void bwd_blocks(const QkNorm& a, int lanes, int& qb, int& kb) {
-  const int64_t cap = max_blocks(), per = kWarps * (32 / lanes);
-  const int64_t qi = nblk(a.rows * a.q.n, per), ki = nblk(a.rows * a.k.n, per);
-  if (qi + ki <= cap) {
-    qb = (int)qi;
-    kb = (int)ki;
-  } else {
-    kb = a.k.n ? (int)imax(1, cap * ki / (qi + ki)) : 0;
-    qb = (int)(cap - kb);
-  }
-}
-
 // whether the tensor's rows keep accesses of four elements (eight: bf16 forward) aligned
 bool vec_ok(const QkNormHeads& h, int dt, bool backward) {
   auto al = [](const void* p) { return ((uintptr_t)p & 15) == 0; };
@@ -477,6 +473,21 @@ bool vec_ok(const QkNormHeads& h, int dt, bool backward) {
 bool vec_ok(const QkNorm& a, bool backward) {
   return a.hd % (a.dt == DT_BF16 && !backward ? 16 : 8) == 0 && vec_ok(a.q, a.dt, backward) &&
          vec_ok(a.k, a.dt, backward);
+}
+
+// blocks of the backward for the queries and the keys, in proportion to their heads; one wave
+void bwd_blocks(const QkNorm& a, int& qb, int& kb) {
+  const bool vec = vec_ok(a, true);
+  const int64_t cap = (int64_t)sm_count() * bwd_blocks_per_sm(a.dt == DT_BF16, vec);
+  const int64_t per = kWarps * (32 / lanes_of(a.hd, vec));
+  const int64_t qi = nblk(a.rows * a.q.n, per), ki = nblk(a.rows * a.k.n, per);
+  if (qi + ki <= cap) {
+    qb = (int)qi;
+    kb = (int)ki;
+  } else {
+    kb = a.k.n ? (int)imax(1, cap * ki / (qi + ki)) : 0;
+    qb = (int)(cap - kb);
+  }
 }
 
 template <typename T>
@@ -559,12 +570,12 @@ cudaError_t qk_norm_rope_fwd(const QkNorm& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-size_t qk_norm_bwd_partial_floats(int64_t hd) { return (size_t)max_blocks() * hd; }
+size_t qk_norm_bwd_partial_floats(int64_t hd) { return (size_t)sm_count() * kBwdBlocks * hd; }
 
 cudaError_t qk_norm_rope_bwd(const QkNorm& a, float* dq_g, float* dk_g, float* partial,
                              cudaStream_t st) {
   Backward b;
-  bwd_blocks(a, lanes_of(a.hd, vec_ok(a, true)), b.qb, b.kb);
+  bwd_blocks(a, b.qb, b.kb);
   b.partial = partial;
   if (a.dt == DT_BF16)
     launch_type<__nv_bfloat16, true>(a, b, st);
