@@ -442,8 +442,14 @@ qk_gain_kernel(int hd, int q_blocks, int blocks, const float* partial,
   float s = 0.f;
   await_previous();
   if (c < hd) {
-#pragma unroll 8
-    for (int b = b0 + wid; b < b1; b += 32) s += partial[(int64_t)b * hd + c];
+    for (int b = b0 + wid; b < b1; b += 8 * 32) {      // eight loads in flight, always
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = b + 32 * i < b1 ? partial[(int64_t)(b + 32 * i) * hd + c] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
   }
   red[wid][lane] = s;
   __syncthreads();
