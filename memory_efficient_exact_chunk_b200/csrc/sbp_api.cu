@@ -112,7 +112,10 @@ struct LayerPlan {
   float *dKp, *dVp;
   void *xg, *n1, *q, *o, *n2, *gu, *m, *dgu, *dO;
   float *dyg, *rstd1, *qkv, *alse, *hbuf, *rstd2, *dn2, *dh, *delta, *dq, *dn1, *dxg;
-  float *dkpre, *dvg, *rpart, *cpart;
+  float *dkpre, *dvg, *rpart;
+  // the column sums' partials: the query bias is summed on a side stream, in reverse order while
+  // the caller's stream sums those of keys and values
+  float *cpart_q, *cpart_kv;
   int* aflags;   // the attention forward's split flags (its partials use dq and delta)
   // with query/key norms: the chunk's projections before the norm, the values before they go to
   // the prefix, the blocks' partial gain gradients
@@ -170,8 +173,8 @@ void layer_carve(Carver& c, const sbp_layer_cfg& L, LayerPlan& p, bool qk_norm =
   p.dvg = c.take<float>((size_t)R * dkv);
   p.rpart = c.take<float>(rmsnorm_bwd_partial_floats(d));
   p.aflags = c.take<int>(attn_fwd_split_flags(B, chunk_max(T, L.num_chunks), L.n_heads));
-  int64_t wmax = dq > dkv ? dq : dkv;
-  p.cpart = c.take<float>(colsum_partial_floats(wmax));
+  p.cpart_q = c.take<float>(colsum_partial_floats(dq));
+  p.cpart_kv = c.take<float>(colsum_partial_floats(dkv));
   p.dyg16 = p.dh16 = p.dq16 = p.khi = p.klo = p.vhi = p.vlo = nullptr;
   if (dt == DT_BF16) {
     p.dyg16 = c.take_bytes((size_t)R * d * 2);
@@ -927,8 +930,8 @@ static sbp_status layer_backward_run(const sbp_layer_cfg* cfg, const sbp_layer_w
                                       DT_F32, gr->wv, d, EPI_ACC)), st));
     }
     if (has_bias) {
-      SBP_CK(colsum_acc(R, dkv, p.dkpre, gr->bk, p.cpart, st));
-      SBP_CK(colsum_acc(R, dkv, p.dvg, gr->bv, p.cpart, st));
+      SBP_CK(colsum_acc(R, dkv, p.dkpre, gr->bk, p.cpart_kv, st));
+      SBP_CK(colsum_acc(R, dkv, p.dvg, gr->bv, p.cpart_kv, st));
     }
     return SBP_OK;
   };
@@ -1040,7 +1043,7 @@ static sbp_status layer_backward_run(const sbp_layer_cfg* cfg, const sbp_layer_w
     SBP_CK(fork_to(1, 11));
     SBP_CK(gemm(over_tokens(mk_gemm(dq, d, R, dQdt, dQ, true, dq, dt, p.n1, false, d, DT_F32,
                                     gr->wq, d, EPI_ACC)), s1));
-    if (has_bias) SBP_CK(colsum_acc(R, dq, p.dq, gr->bq, p.cpart, s1));
+    if (has_bias) SBP_CK(colsum_acc(R, dq, p.dq, gr->bq, p.cpart_q, s1));
     SBP_CK(gemm(mk_gemm(R, d, dq, dQdt, dQ, false, dq, dt, w->wq, false, d, DT_F32, p.dn1, d,
                         EPI_STORE), st));
     // in reverse order this chunk's dK/dV rows are final: its K/V part joins dn1 here
