@@ -912,13 +912,6 @@ cudaError_t sort_by_id(int64_t rows, int64_t vocab, const int* ids, const Plan& 
            (int)rows, (int)vocab, ids, p.sorted, p.head, a.n_long);
     return cudaGetLastError();
   }
-  const int per_block = (int)deal_rows(rows);
-  const dim3 grid((unsigned)nblk(rows, per_block));
-  int* base = p.head;
-  launch(embed_count_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block, (int)vocab,
-         ids, p.counts, a.n_long);
-  launch_next(embed_deal_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block,
-              (int)vocab, ids, (const int*)p.counts, p.dealt, base);
   const int bins = (int)((vocab - 1) / kBuckets + 1);
   // 512 threads where a frequent id may fill a bucket with thousands of rows (64K rows: 502 us in
   // all, 505 with 256; 8570 rows: 26.5, 25.9)
@@ -926,11 +919,20 @@ cudaError_t sort_by_id(int64_t rows, int64_t vocab, const int* ids, const Plan& 
   int warps = threads / 32;      // as many histograms as 96 KB hold
   while (warps > 1 && (size_t)bins * (warps + 2) * 4 > 96 * 1024) warps /= 2;
   const size_t smem = sizeof(int) * (size_t)bins * (warps + 2);
-  if (smem > 48 * 1024) {
+  // asked for below 48 KB already, which have to hold the kernel's static arrays too; before the
+  // first launch, as it may fail
+  if (smem > 47 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
         embed_bucket_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
     if (e != cudaSuccess) return e;
   }
+  const int per_block = (int)deal_rows(rows);
+  const dim3 grid((unsigned)nblk(rows, per_block));
+  int* base = p.head;
+  launch(embed_count_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block, (int)vocab,
+         ids, p.counts, a.n_long);
+  launch_next(embed_deal_kernel, grid, dim3(kDealThreads), 0, st, (int)rows, per_block,
+              (int)vocab, ids, (const int*)p.counts, p.dealt, base);
   launch_next(embed_bucket_kernel, dim3(kBuckets), dim3(threads), smem, st, (int)vocab, bins,
               warps, (const int*)base, (const int2*)p.dealt, p.sorted,
               a.accumulate ? static_cast<unsigned char*>(nullptr) : p.present);

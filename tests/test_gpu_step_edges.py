@@ -59,3 +59,39 @@ def test_bias_sums_of_both_chunk_orders_while_the_weight_products_lag(norms):
         again = layer_run(L, W, x, dy, 2, reverse=True)
         for n, v in first.items():
             assert torch.equal(v, again[n]), n
+
+
+# ------------------------------------------------------------------------------- embedding
+NEAR_THE_DEFAULT = """
+import torch
+from memory_efficient_exact_chunk_b200 import sbp
+rows, vocab = {rows}, {vocab}
+g = torch.Generator(device="cuda").manual_seed(1)
+ids = torch.randint(0, vocab, (rows,), generator=g, device="cuda", dtype=torch.int32)
+ids[:3] = torch.tensor([0, vocab - 1, vocab], dtype=torch.int32, device="cuda")
+dy = torch.randn(rows, 4, generator=g, device="cuda")
+d = torch.empty(vocab, 4, device="cuda")
+sbp.embedding_scaled_backward(ids, dy, 1.0, d, accumulate=False)
+ok = ids < vocab
+i, v = ids[ok].long(), dy[ok].double()
+z = torch.zeros(vocab, 4, dtype=torch.float64, device="cuda")
+want, mag = z.index_add(0, i, v), z.index_add(0, i, v.abs())
+n = torch.bincount(i, minlength=vocab)[:, None]
+# a sum of n terms and the product with the scale
+assert ((d.double() - want).abs() <= mag * (n + 1) * 2.0 ** -24).all()
+"""
+
+
+@pytest.mark.parametrize("rows,vocab", [(40000, 349184), (40000, 348673), (5000, 628736),
+                                        (5000, 628225), (40000, 348672), (5000, 628737)])
+def test_embedding_gradient_with_histograms_next_to_48_kb(rows, vocab):
+    """The sort's histograms of these tables fill the 48 KB that a CTA may have without asking,
+    to the last bytes.  A process of its own: an earlier call with a larger table would have asked
+    already."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", NEAR_THE_DEFAULT.format(rows=rows, vocab=vocab)],
+                       cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
