@@ -38,7 +38,9 @@ class Workspaces:
 
 
 def _layer_ws(cfg: sbp.LayerCfg, layers: List[dict], ws: Workspaces):
-    return ws.get("layer", sbp.layer_workspace_size(cfg, any(map(sbp.has_qk_norm, layers))))
+    # of the kinds that occur, either may need the larger one
+    kinds = {sbp.has_qk_norm(W) for W in layers} or {False}
+    return ws.get("layer", max(sbp.layer_workspace_size(cfg, k) for k in kinds))
 
 
 def stack_forward(cfg: sbp.LayerCfg, embed, layers: List[dict], final_g, ids, ws: Workspaces,
