@@ -81,7 +81,9 @@ sbp_status sbp_qk_norm_rope_forward(const sbp_qk_cfg* cfg, const void* q, int64_
  * inverse rotation of the upstream gradient and xhat = x / sqrt(mean(x^2) + eps),
  *   dg += sum over rows and heads of u * xhat       (accumulated)
  *   dx  = (g u - xhat * mean(xhat * g u)) / sqrt(mean(x^2) + eps)      (overwritten)
- * dq_out / dk_out (upstream), dq / dk and the gain gradients dq_g / dk_g are fp32. */
+ * dq_out / dk_out (upstream), dq / dk and the gain gradients dq_g / dk_g are fp32.  dq_g and dk_g
+ * may be one vector (a gain that queries and keys share), which then receives both sums; they
+ * must not overlap in part. */
 size_t sbp_qk_norm_rope_backward_workspace_size(const sbp_qk_cfg* cfg);
 sbp_status sbp_qk_norm_rope_backward(const sbp_qk_cfg* cfg, const void* q, int64_t ldq,
                                      const void* k, int64_t ldk, const void* q_g, const void* k_g,

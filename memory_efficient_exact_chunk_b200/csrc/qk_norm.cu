@@ -431,7 +431,8 @@ qk_bwd_kernel(int rows, int hd, float inv_hd, int q_blocks, Heads<T> q, Heads<T>
 }
 
 // dst[c] += sum of the blocks' partials, 32 columns of the queries' (y = 0) or the keys' (y = 1)
-// gain per CTA: each warp adds a 32nd of the partials, warp 0 the 32 sums in order.
+// gain per CTA: each warp adds a 32nd of the partials, warp 0 the 32 sums in order.  Where both
+// have one gradient, y = 0 adds the partials of all blocks.
 __global__ void __launch_bounds__(1024)
 qk_gain_kernel(int hd, int q_blocks, int blocks, const float* partial,
                float* __restrict__ dq_g, float* __restrict__ dk_g) {
@@ -587,8 +588,9 @@ cudaError_t qk_norm_rope_bwd(const QkNorm& a, float* dq_g, float* dk_g, float* p
     launch_type<__nv_bfloat16, true>(a, b, st);
   else
     launch_type<float, true>(a, b, st);
-  launch_next(qk_gain_kernel, dim3((unsigned)nblk(a.hd, 32), b.kb ? 2 : 1), dim3(1024), 0, st,
-         (int)a.hd, b.qb, b.qb + b.kb, (const float*)partial, dq_g, dk_g);
+  const bool apart = b.kb > 0 && dk_g != dq_g;
+  launch_next(qk_gain_kernel, dim3((unsigned)nblk(a.hd, 32), apart ? 2 : 1), dim3(1024), 0, st,
+         (int)a.hd, apart ? b.qb : b.qb + b.kb, b.qb + b.kb, (const float*)partial, dq_g, dk_g);
   return cudaGetLastError();
 }
 

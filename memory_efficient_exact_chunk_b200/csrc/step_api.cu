@@ -30,6 +30,12 @@ sbp_status fail(sbp_status s, const char* fmt, ...) {
 
 inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+// whether two ranges of n bytes have bytes in common
+inline bool overlap(const void* p, const void* q, size_t n) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  return a < b + n && b < a + n;
+}
+
 sbp_status check_ws(void* ws, size_t have, size_t need) {
   if (!ws) return fail(SBP_ERR_INVALID_ARG, "workspace is NULL");
   if (!aligned(ws, 256)) return fail(SBP_ERR_INVALID_ARG, "workspace not 256-byte aligned");
@@ -240,6 +246,8 @@ sbp_status sbp_qk_norm_rope_backward(const sbp_qk_cfg* cfg, const void* q, int64
   if (sbp_status s = check_out(a.k, a.hd, dk, lddk, 4)) return s;
   if (!dq_g || !aligned(dq_g, 4) || (a.k.n && (!dk_g || !aligned(dk_g, 4))))
     return fail(SBP_ERR_INVALID_ARG, "a gain gradient is NULL or misaligned");
+  if (a.k.n && dq_g != dk_g && overlap(dq_g, dk_g, sizeof(float) * a.hd))
+    return fail(SBP_ERR_INVALID_ARG, "dq_g and dk_g overlap in part");
   if (sbp_status s = check_ws(workspace, workspace_bytes,
                               sbp_qk_norm_rope_backward_workspace_size(cfg)))
     return s;

@@ -607,7 +607,8 @@ def qk_norm_rope_forward(q, k, q_g, k_g, cos, sin, eps, q_out, k_out, positions=
 def qk_norm_rope_backward(q, k, q_g, k_g, cos, sin, eps, dq_out, dk_out, dq, dk, dq_g, dk_g,
                           positions=None, seq_len=None, ws=None, stream=None):
     """Backward of qk_norm_rope_forward from its inputs: dq, dk overwritten (they may be dq_out,
-    dk_out), dq_g, dk_g accumulated; all gradients fp32.  Returns the workspace."""
+    dk_out), dq_g, dk_g accumulated (one vector may be both, of a gain that is shared); all
+    gradients fp32.  Returns the workspace."""
     f32 = _torch().float32
     args = _qk_call(q, k, q_g, k_g, cos, sin, eps, positions, seq_len)
     gain = (q.shape[2],)

@@ -95,3 +95,86 @@ def test_embedding_gradient_with_histograms_next_to_48_kb(rows, vocab):
     r = subprocess.run([sys.executable, "-c", NEAR_THE_DEFAULT.format(rows=rows, vocab=vocab)],
                        cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+# ---------------------------------------------------------------------- the gains' gradients
+def gain_sums(x, dy, eps):
+    """sum over rows and heads of dy * xhat at position 0 (where the rotation is the identity),
+    and of its magnitude, in fp64."""
+    x = x.double()
+    xh = x / (x.square().mean(-1, keepdim=True) + eps).sqrt()
+    t = xh * dy.double()
+    return t.sum((0, 1)), t.abs().sum((0, 1))
+
+
+def gain_chain(heads, hd):
+    """Additions between a summand of a gain's gradient and the result, at most: the heads that a
+    lane adds one after the other (at least 4 CTAs of 4 warps per SM share them, of which a tensor
+    gets at least half of its part), the heads of a warp, the 4 warps of a CTA, the partial rows (of
+    at most 5 CTAs per SM) per warp of the joining CTA, its 32 warps, the old value."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    per_warp = 32 // max(1, 2 ** int(np.ceil(np.log2(hd / 16))))
+    lane = 2 * -(-heads // (sms * 4 * 4 * per_warp))
+    return lane + 31 + 3 + -(-sms * 5 // 32) + 31 + 1
+
+
+def gain_close(got, want, mag, heads, hd):
+    # a summand: the norm's factor (hd / 2 + 8), the rotation (a product that is exact at position 0
+    # and a sum with zero) and two products
+    bound = mag * (gain_chain(heads, hd) + hd / 2 + 12) * E + want.abs() * E
+    err = (got.double() - want).abs()
+    assert (err <= bound).all(), float((err - bound).max())
+
+
+@pytest.mark.parametrize("rows,H,Hkv,hd,dt", [
+    (3001, 28, 4, 80, "bf16"), (20011, 28, 4, 128, "bf16"), (4099, 12, 12, 96, "f32"),
+    (9001, 8, 8, 10, "f32"), (2050, 32, 8, 128, "f32"), (3, 2, 1, 64, "bf16"), (700, 1, 300, 16, "bf16")])
+def test_gain_gradients_lose_no_summand(rows, H, Hkv, hd, dt):
+    """Sums of up to 600 thousand heads to within the roundings of their own additions: the queries
+    alone (as the layer calls it), the queries with the keys, and one gain that both share."""
+    g = gen(rows)
+    x = {n: torch.randn(rows, h, hd, generator=g, device="cuda").to(DT[dt])
+         for n, h in (("q", H), ("k", Hkv))}
+    dy = {n: torch.randn(v.shape, generator=g, device="cuda") for n, v in x.items()}
+    gain = (1 + 0.3 * torch.randn(hd, generator=g, device="cuda")).to(DT[dt])
+    cos, sin = sbp.rope_table(1, hd, 1e4)
+    want = {n: gain_sums(x[n], dy[n], 1e-6) for n in x}
+    dx = {n: torch.empty_like(v) for n, v in dy.items()}
+
+    def run(k, dq_g, dk_g):
+        on = lambda t: t if k else None
+        sbp.qk_norm_rope_backward(x["q"], on(x["k"]), gain, on(gain), cos, sin, 1e-6, dy["q"],
+                                  on(dy["k"]), dx["q"], on(dx["k"]), dq_g, on(dk_g), seq_len=1)
+    zero = lambda: torch.zeros(hd, device="cuda")
+    a, b, c, shared = zero(), zero(), zero(), zero()
+    run(False, a, None)
+    gain_close(a, *want["q"], rows * H, hd)
+    run(True, b, c)
+    gain_close(b, *want["q"], rows * (H + Hkv), hd)
+    gain_close(c, *want["k"], rows * (H + Hkv), hd)
+    for _ in range(3):
+        shared.fill_(0.0)
+        run(True, shared, shared)
+        gain_close(shared, want["q"][0] + want["k"][0], want["q"][1] + want["k"][1],
+                   rows * (H + Hkv), hd)
+
+
+# ------------------------------------------------------------- stacks of both kinds of layers
+def test_stack_of_layers_with_and_without_norms():
+    """bf16, head width 64: the layers without norms need the larger workspace there."""
+    from memory_efficient_exact_chunk_b200 import stack
+    L, T, V = S(128, 4, 2, 64, 256, 1e-6, 10000.0), 1024, 61
+    layers = [layer_data(L, 1, 1, "bf16", i, norms)[0] for i, norms in enumerate((True, False))]
+    cfg = sbp.layer_cfg(1, T, L.d_model, L.n_heads, L.n_kv_heads, L.head_dim, L.ffn, L.rms_eps,
+                        L.rope_theta, sbp.SBP_BF16, 2)
+    assert sbp.layer_workspace_size(cfg) > sbp.layer_workspace_size(cfg, True)
+    table = (torch.randn(V, L.d_model, generator=gen(9), device="cuda") * 0.05).bfloat16()
+    ids = torch.arange(T, device="cuda", dtype=torch.int32) * 7 % V
+    w = torch.full((T,), 1.0 / T, device="cuda")
+    fg = torch.ones(L.d_model, dtype=torch.bfloat16, device="cuda")
+    got = [stack.stack_backward(cfg, table, order, fg, table, ids, ids, w, embed_scale=2.0)
+           for order in (layers, layers[::-1])]
+    for r in got:
+        assert torch.isfinite(r.loss).all()
+        assert all(torch.isfinite(t).all() and (t != 0).any()
+                   for t in stack.grad_tensors(r.grads))

@@ -25,3 +25,26 @@ def test_a_stack_of_both_kinds_of_layers_gets_the_larger_workspace(lib, head_dim
                          ([{}], sizes[0]), ([normed, normed], sizes[1])):
         ws = stack.Workspaces("cpu")
         assert stack._layer_ws(cfg, layers, ws).numel() == max(need, 256)
+
+
+# ---------------------------------------------------------------------------- queries and keys
+FAKE = 0x100000  # an aligned address that is never dereferenced (argument checks fail first)
+
+
+def test_gain_gradients_that_overlap_in_part_are_refused(lib):
+    """One vector for both gains is allowed, one that begins inside the other is not (the workspace
+    of none, which is checked behind it, keeps the allowed calls from a launch)."""
+    import ctypes as C
+    cfg = sbp.QkCfg(4, 4, 2, 16, 4, 8, 1e-6, 1)
+
+    def call(dqg, dkg):
+        code = lib.sbp_qk_norm_rope_backward(
+            C.byref(cfg), FAKE, 64, FAKE, 32, FAKE, FAKE, None, FAKE, FAKE, FAKE, 64, FAKE, 32,
+            FAKE, 64, FAKE, 32, dqg, dkg, None, 0, None)
+        return code, lib.sbp_last_error().decode()
+    for dqg, dkg in ((FAKE, FAKE + 4), (FAKE + 60, FAKE)):
+        code, msg = call(dqg, dkg)
+        assert code == 1 and "overlap" in msg
+    for dqg, dkg in ((FAKE, FAKE), (FAKE, FAKE + 64), (FAKE + 64, FAKE)):
+        code, msg = call(dqg, dkg)
+        assert code == 1 and "workspace" in msg
