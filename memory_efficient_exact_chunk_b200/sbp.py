@@ -7,6 +7,7 @@ is missing, ``load()`` raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 from typing import Dict, Optional
@@ -209,10 +210,18 @@ def _dtype_code(t):
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
-def workspace(nbytes: int, device="cuda"):
-    """A 256-byte aligned device buffer of at least nbytes (torch allocations are aligned)."""
+def allocating(stream):
+    """Where torch allocates for `stream` (None: the current stream).  Memory taken from another
+    stream's pool may still be in use by that stream's queued work."""
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+
+def workspace(nbytes: int, device="cuda", stream=None):
+    """A 256-byte aligned device buffer of at least nbytes (torch allocations are aligned) for
+    calls on `stream`."""
     torch = _torch()
-    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    with allocating(stream):
+        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
 def device_status(ws, stream=None):
@@ -232,7 +241,7 @@ def lmhead_ce_backward(hidden_states, weight, targets, loss_weights, num_chunks,
     dt = _dtype_code(hidden_states)
     need = lmhead_ce_workspace_size(N, d, V, num_chunks, dt)
     if ws is None:
-        ws = workspace(need, hidden_states.device)
+        ws = workspace(need, hidden_states.device, stream)
     _check(load().sbp_lmhead_ce_backward_stream(
         N, d, V, num_chunks, dt, _ptr(hidden_states), _ptr(weight), _ptr(targets),
         _ptr(loss_weights), _ptr(loss_out), _ptr(d_hidden), _ptr(d_weight), _ptr(ws),
@@ -249,7 +258,7 @@ def lmhead_ce_backward_host(hidden_states_host, weight, targets_host, loss_weigh
     dt = _dtype_code(hidden_states_host)
     if ws is None:
         ws = workspace(int(load().sbp_lmhead_ce_workspace_size_host(N, d, V, num_chunks, dt)),
-                       weight.device)
+                       weight.device, stream)
     _check(load().sbp_lmhead_ce_backward_stream_host(
         N, d, V, num_chunks, dt, _ptr(hidden_states_host), _ptr(weight), _ptr(targets_host),
         _ptr(loss_weights_host), _ptr(loss_out), _ptr(d_hidden), _ptr(d_weight), _ptr(ws),
@@ -270,7 +279,7 @@ def lmhead_ce_forward(hidden_states, weight, targets, loss_weights, num_chunks, 
     dt = _dtype_code(hidden_states)
     need = lmhead_ce_workspace_size(N, d, V, num_chunks, dt)
     if ws is None:
-        ws = workspace(need, hidden_states.device)
+        ws = workspace(need, hidden_states.device, stream)
     _check(load().sbp_lmhead_ce_forward_stream(
         N, d, V, num_chunks, dt, _ptr(hidden_states), _ptr(weight), _ptr(targets),
         _ptr(loss_weights), _ptr(token_ce), _ptr(loss_out) if loss_out is not None else None,
@@ -286,7 +295,7 @@ def dpo_token_weights(n_pairs, seq_len, token_ce, response_mask, ref_logp, beta,
                       weights, seq_logp=None, ws=None, stream=None):
     """DPO loss into loss_out[0] and per-token loss weights (include/sbp_dpo.h)."""
     if ws is None:
-        ws = workspace(dpo_workspace_size(n_pairs), token_ce.device)
+        ws = workspace(dpo_workspace_size(n_pairs), token_ce.device, stream)
     _check(load().sbp_dpo_token_weights(
         n_pairs, seq_len, _ptr(token_ce), _ptr(response_mask), _ptr(ref_logp), float(beta),
         _ptr(loss_out), _ptr(seq_logp) if seq_logp is not None else None, _ptr(weights),
@@ -333,11 +342,11 @@ def layer_workspace_size(cfg: LayerCfg, qk_norm: bool = False) -> int:
     return lib.sbp_decoder_layer_workspace_size(C.byref(cfg))
 
 
-def _layer_ws(cfg, qk_norm, ws, device):
+def _layer_ws(cfg, qk_norm, ws, device, stream):
     need = layer_workspace_size(cfg, qk_norm)
     if need == 0:
         raise SbpError(1, "invalid layer configuration")
-    return workspace(need, device) if ws is None else ws
+    return workspace(need, device, stream) if ws is None else ws
 
 
 def _qk_gains(cfg, weights, device):
@@ -353,7 +362,7 @@ def _qk_gains(cfg, weights, device):
 def _layer_backward(reverse, cfg, weights, x, dy, dx, grads, ws, stream):
     lib = load()
     qk_norm = has_qk_norm(weights)
-    ws = _layer_ws(cfg, qk_norm, ws, x.device)
+    ws = _layer_ws(cfg, qk_norm, ws, x.device, stream)
     w = _struct(LayerWeights, weights)
     g = _struct(LayerGrads, grads)
     if qk_norm:
@@ -390,7 +399,7 @@ def decoder_layer_backward_reverse(cfg: LayerCfg, weights, x, dy, dx, grads, ws=
 def decoder_layer_forward(cfg: LayerCfg, weights, x, y, ws=None, stream=None):
     lib = load()
     qk_norm = has_qk_norm(weights)
-    ws = _layer_ws(cfg, qk_norm, ws, x.device)
+    ws = _layer_ws(cfg, qk_norm, ws, x.device, stream)
     w = _struct(LayerWeights, weights)
     if qk_norm:
         gains = _qk_gains(cfg, weights, x.device)
@@ -414,7 +423,7 @@ def rmsnorm_backward(x2d, g, rstd, dy2d, dx2d, dg, accumulate=False, ws=None, st
     rows, cols = x2d.shape
     need = load().sbp_rmsnorm_backward_workspace_size(rows, cols)
     if ws is None or ws.numel() < need:
-        ws = workspace(need, x2d.device)
+        ws = workspace(need, x2d.device, stream)
     _check(load().sbp_rmsnorm_backward(rows, cols, _dtype_code(x2d), _ptr(x2d), _ptr(g),
                                        _ptr(rstd), _ptr(dy2d), _ptr(dx2d), int(accumulate),
                                        _ptr(dg), _ptr(ws), ws.numel(), _stream(stream)))
@@ -433,7 +442,7 @@ def embedding_backward(ids, dy2d, d_table, ws=None, stream=None):
     V, cols = d_table.shape
     need = load().sbp_embedding_backward_workspace_size(rows, V)
     if ws is None or ws.numel() < need:
-        ws = workspace(need, dy2d.device)
+        ws = workspace(need, dy2d.device, stream)
     _check(load().sbp_embedding_backward(rows, cols, V, _ptr(ids), _ptr(dy2d), _ptr(d_table),
                                          _ptr(ws), ws.numel(), _stream(stream)))
     return ws
@@ -480,9 +489,7 @@ def _with_ws(ws, dev, stream, need, call):
             return ws
         if code != 3:                    # SBP_ERR_WORKSPACE, before anything is queued
             _check(code)
-    ws = workspace(need(), f"cuda:{dev}")
-    if stream is not None:               # allocated for the current stream, used on this one
-        ws.record_stream(stream)
+    ws = workspace(need(), f"cuda:{dev}", stream)
     _check(call(ws.data_ptr(), ws.nbytes))
     return ws
 
@@ -535,8 +542,9 @@ def rope_table(n_positions, head_dim, theta, device="cuda", stream=None):
     torch = _torch()
     if n_positions < 1 or head_dim < 2:
         raise ValueError("rope_table: need positive sizes")
-    cos = torch.empty(n_positions, head_dim // 2, dtype=torch.float32, device=device)
-    sin = torch.empty_like(cos)
+    with allocating(stream):
+        cos = torch.empty(n_positions, head_dim // 2, dtype=torch.float32, device=device)
+        sin = torch.empty_like(cos)
     _, st = _on_device(stream, cos)
     _check(load().sbp_rope_table(n_positions, head_dim, theta, cos.data_ptr(), sin.data_ptr(),
                                  st))

@@ -178,3 +178,28 @@ def test_stack_of_layers_with_and_without_norms():
         assert torch.isfinite(r.loss).all()
         assert all(torch.isfinite(t).all() and (t != 0).any()
                    for t in stack.grad_tensors(r.grads))
+
+
+# ------------------------------------------------------------------------------------ streams
+def test_workspaces_of_calls_on_another_stream():
+    """While the current stream has yet to write to memory that its pool has back, a call on another
+    stream without a workspace gets memory of its own."""
+    rows, cols, vocab = 9000, 40, 3000
+    g = gen(5)
+    ids = torch.randint(0, vocab, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    dy = torch.randn(rows, cols, generator=g, device="cuda")
+    want, got = torch.empty(vocab, cols, device="cuda"), torch.zeros(vocab, cols, device="cuda")
+    need = sbp.embedding_scaled_backward(ids, dy, 1.5, want, accumulate=False).numel()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        torch.cuda._sleep(2_000_000)          # about a millisecond
+        late = torch.empty(need, dtype=torch.uint8, device="cuda").fill_(255)
+        at = late.data_ptr()
+        del late
+        ws = sbp.embedding_scaled_backward(ids, dy, 1.5, got, accumulate=False, stream=side)
+        assert ws.data_ptr() != at
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        got.zero_()
+        torch.cuda.synchronize()

@@ -48,3 +48,57 @@ def test_gain_gradients_that_overlap_in_part_are_refused(lib):
     for dqg, dkg in ((FAKE, FAKE), (FAKE, FAKE + 64), (FAKE + 64, FAKE)):
         code, msg = call(dqg, dkg)
         assert code == 1 and "workspace" in msg
+
+
+# ------------------------------------------------------------------------------------ streams
+class _Streams:
+    """torch.cuda.stream without a GPU: keeps the stream that allocations are made for."""
+
+    def __init__(self, monkeypatch):
+        self.now, self.made = None, []
+        monkeypatch.setattr(torch.cuda, "stream", self.use)
+        empty = torch.empty
+        monkeypatch.setattr(torch, "empty", lambda *a, **k: (
+            self.made.append(self.now), empty(*a, **{**k, "device": "cpu"}))[1])
+
+    def use(self, stream):
+        import contextlib
+
+        @contextlib.contextmanager
+        def on():
+            before, self.now = self.now, stream
+            yield
+            self.now = before
+        return on()
+
+
+def test_workspaces_are_allocated_for_the_stream_they_are_used_on(monkeypatch):
+    """The current stream's queued work may still use memory that its pool hands out again."""
+    streams = _Streams(monkeypatch)
+    need = lambda: 1000
+    calls = []
+    call = lambda p, n: calls.append(n) or 0
+    sbp._with_ws(None, 0, "side", need, call)
+    sbp._with_ws(None, 0, None, need, call)
+    assert streams.made == ["side", None] and calls == [1000, 1000]
+    # one that is too small is replaced by one for the stream
+    small = torch.zeros(8, dtype=torch.uint8)
+    monkeypatch.setattr(type(small), "get_device", lambda t: 0, raising=False)
+    sbp._with_ws(small, 0, "side", need, lambda p, n: 3 if n < 1000 else 0)
+    assert streams.made[2:] == ["side"]
+    # the calls of sbp.h too; the library is a fake that takes everything
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: 512 if name.endswith("size") else 0
+    monkeypatch.setattr(sbp, "load", Lib)
+    monkeypatch.setattr(sbp, "_stream", lambda s: None)
+    x = torch.zeros(2, 2)
+    del streams.made[:]
+    sbp.rmsnorm_backward(x, x, x, x, x, x, stream="side")
+    sbp.embedding_backward(torch.zeros(2, dtype=torch.int32), x, x, stream="side")
+    sbp.lmhead_ce_backward(x, x, x, x, 1, x, x, x, stream="side")
+    sbp.lmhead_ce_forward(x, x, x, x, 1, x, stream="side")
+    cfg = sbp.layer_cfg(1, 4, 4, 1, 1, 2, 4, 1e-6, 1e4, sbp.SBP_F32, 1)
+    sbp.decoder_layer_forward(cfg, {}, x, x, stream="side")
+    sbp.decoder_layer_backward(cfg, {}, x, x, x, {}, stream="side")
+    assert streams.made == ["side"] * 6
