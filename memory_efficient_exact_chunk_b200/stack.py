@@ -5,10 +5,13 @@ The forward keeps only each layer's input (the layer-wise checkpoints StreamBP b
 skill page "StreamBP: Memory-Efficient Backpropagation", Core Concept and Architecture
 Overview, Layer-Wise Application).  The backward runs the LM-head CE and every layer through
 the streamed entry points with the same D.  Every arithmetic step runs in libsbp kernels; this
-module only allocates buffers and orders the calls.
+module only allocates buffers and orders the calls.  With `stream` all of that happens on that
+stream; arguments that another stream fills have to be ready for it.
 """
 from __future__ import annotations
 
+import functools
+import inspect
 from dataclasses import dataclass
 from typing import Dict, List
 
@@ -37,12 +40,25 @@ class Workspaces:
         return t
 
 
+def _on_its_stream(fn):
+    """fn with its `stream`, where one is given, as the current one: what fn allocates, clears and
+    hands to `on_final` then belongs to the stream that its library calls are queued on."""
+    places = inspect.signature(fn)
+
+    @functools.wraps(fn)
+    def run(*args, **kwargs):
+        with sbp.allocating(places.bind(*args, **kwargs).arguments.get("stream")):
+            return fn(*args, **kwargs)
+    return run
+
+
 def _layer_ws(cfg: sbp.LayerCfg, layers: List[dict], ws: Workspaces):
     # of the kinds that occur, either may need the larger one
     kinds = {sbp.has_qk_norm(W) for W in layers} or {False}
     return ws.get("layer", max(sbp.layer_workspace_size(cfg, k) for k in kinds))
 
 
+@_on_its_stream
 def stack_forward(cfg: sbp.LayerCfg, embed, layers: List[dict], final_g, ids, ws: Workspaces,
                   stream=None, embed_scale=None):
     """Embedding and L chunked layer forwards; returns the layer inputs (checkpoints), the
@@ -68,6 +84,7 @@ def stack_forward(cfg: sbp.LayerCfg, embed, layers: List[dict], final_g, ids, ws
     return xs, hf, rstd
 
 
+@_on_its_stream
 def stack_backward_from(cfg: sbp.LayerCfg, layers: List[dict], final_g, lm_w, ids, targets,
                         loss_weights, xs, hf, rstd, ws: Workspaces, grads=None, stream=None,
                         on_final=None, embed_scale=None):
@@ -140,6 +157,7 @@ def zero_grads(layers, lm_w, final_g, dev, embed_shape=None):
     return g
 
 
+@_on_its_stream
 def stack_backward(cfg: sbp.LayerCfg, embed, layers: List[dict], final_g, lm_w, ids, targets,
                    loss_weights, stream=None, keep_workspace: dict | None = None,
                    embed_scale=None, max_grad_norm=None) -> StackResult:
@@ -165,6 +183,7 @@ def stack_backward(cfg: sbp.LayerCfg, embed, layers: List[dict], final_g, lm_w, 
     return res
 
 
+@_on_its_stream
 def stack_dpo_step(cfg: sbp.LayerCfg, embed, layers: List[dict], final_g, lm_w, ids, targets,
                    response_mask, ref_logp, beta: float, ws: Workspaces, grads=None, stream=None,
                    embed_scale=None):

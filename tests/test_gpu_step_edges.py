@@ -203,3 +203,32 @@ def test_workspaces_of_calls_on_another_stream():
         assert torch.equal(got, want)
         got.zero_()
         torch.cuda.synchronize()
+
+
+def test_a_training_step_on_another_stream():
+    """The whole step is on its stream: it does not wait for the current one, which is busy with
+    memory that its pool has back, and its results are those of a step on the current stream."""
+    from memory_efficient_exact_chunk_b200 import stack
+    L, T, V = S(64, 4, 2, 16, 96, 1e-6, 10000.0), 64, 61
+    W, _, _ = layer_data(L, 1, 1, "f32", 2, True)
+    cfg = sbp.layer_cfg(1, T, L.d_model, L.n_heads, L.n_kv_heads, L.head_dim, L.ffn, L.rms_eps,
+                        L.rope_theta, sbp.SBP_F32, 2)
+    table = torch.randn(V, L.d_model, generator=gen(9), device="cuda") * 0.05
+    ids = torch.arange(T, device="cuda", dtype=torch.int32) * 7 % V
+    w = torch.full((T,), 1.0 / T, device="cuda")
+    args = (cfg, table, [W], torch.ones(L.d_model, device="cuda"), table, ids, ids, w)
+    opts = dict(embed_scale=2.0, max_grad_norm=0.05)
+    want = stack.stack_backward(*args, **opts)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda._sleep(20_000_000)         # about ten milliseconds
+        for n in (1 << 8, 1 << 12, 1 << 16, 1 << 20, 1 << 24):
+            torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+        got = stack.stack_backward(*args, **opts, stream=side)
+        side.synchronize()
+        with torch.cuda.stream(side):
+            assert torch.equal(got.loss, want.loss) and torch.equal(got.grad_norm, want.grad_norm)
+            for a, b in zip(stack.grad_tensors(got.grads), stack.grad_tensors(want.grads)):
+                assert torch.equal(a, b)
+        torch.cuda.synchronize()

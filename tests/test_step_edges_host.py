@@ -54,12 +54,17 @@ def test_gain_gradients_that_overlap_in_part_are_refused(lib):
 class _Streams:
     """torch.cuda.stream without a GPU: keeps the stream that allocations are made for."""
 
-    def __init__(self, monkeypatch):
+    def __init__(self, monkeypatch, makers=("empty",)):
         self.now, self.made = None, []
         monkeypatch.setattr(torch.cuda, "stream", self.use)
-        empty = torch.empty
-        monkeypatch.setattr(torch, "empty", lambda *a, **k: (
-            self.made.append(self.now), empty(*a, **{**k, "device": "cpu"}))[1])
+        for name in makers:
+            monkeypatch.setattr(torch, name, self.counted(getattr(torch, name)))
+
+    def counted(self, fn):
+        def make(*a, **k):
+            self.made.append(self.now)
+            return fn(*a, **{**k, "device": "cpu"})
+        return make
 
     def use(self, stream):
         import contextlib
@@ -70,6 +75,13 @@ class _Streams:
             yield
             self.now = before
         return on()
+
+
+class _Taker:
+    """A library that takes every call and does nothing."""
+
+    def __getattr__(self, name):
+        return lambda *a: 512 if name.endswith("size") else 0
 
 
 def test_workspaces_are_allocated_for_the_stream_they_are_used_on(monkeypatch):
@@ -86,14 +98,11 @@ def test_workspaces_are_allocated_for_the_stream_they_are_used_on(monkeypatch):
     monkeypatch.setattr(type(small), "get_device", lambda t: 0, raising=False)
     sbp._with_ws(small, 0, "side", need, lambda p, n: 3 if n < 1000 else 0)
     assert streams.made[2:] == ["side"]
-    # the calls of sbp.h too; the library is a fake that takes everything
-    class Lib:
-        def __getattr__(self, name):
-            return lambda *a: 512 if name.endswith("size") else 0
-    monkeypatch.setattr(sbp, "load", Lib)
-    monkeypatch.setattr(sbp, "_stream", lambda s: None)
+    # the calls of sbp.h too
     x = torch.zeros(2, 2)
     del streams.made[:]
+    monkeypatch.setattr(sbp, "load", _Taker)
+    monkeypatch.setattr(sbp, "_stream", lambda s: None)
     sbp.rmsnorm_backward(x, x, x, x, x, x, stream="side")
     sbp.embedding_backward(torch.zeros(2, dtype=torch.int32), x, x, stream="side")
     sbp.lmhead_ce_backward(x, x, x, x, 1, x, x, x, stream="side")
@@ -102,3 +111,26 @@ def test_workspaces_are_allocated_for_the_stream_they_are_used_on(monkeypatch):
     sbp.decoder_layer_forward(cfg, {}, x, x, stream="side")
     sbp.decoder_layer_backward(cfg, {}, x, x, x, {}, stream="side")
     assert streams.made == ["side"] * 6
+
+
+def test_the_stack_allocates_and_clears_on_its_stream(monkeypatch):
+    """Gradients that the current stream clears are not ready for the calls on another one."""
+    streams = _Streams(monkeypatch, ("empty", "zeros"))
+    monkeypatch.setattr(sbp, "load", _Taker)
+    monkeypatch.setattr(sbp, "_stream", lambda s: None)
+    cfg = sbp.layer_cfg(1, 4, 4, 1, 1, 2, 4, 1e-6, 1e4, sbp.SBP_F32, 1)
+    ids, w = torch.ones(4, dtype=torch.int32), torch.ones(4)
+    table, g = torch.ones(3, 4), torch.ones(4)
+    seen = []
+    stack.stack_backward(cfg, table, [{}], g, table, ids, ids, w, stream="side")
+    assert len(streams.made) > 5 and set(streams.made) == {"side"}
+    del streams.made[:]
+    ws = stack.Workspaces("cpu")
+    xs, hf, rstd = stack.stack_forward(cfg, table, [{}], g, ids, ws, "side")     # by its place
+    stack.stack_backward_from(cfg, [{}], g, table, ids, ids, w, xs, hf, rstd, ws, stream="side",
+                              grads=stack.zero_grads([{}], table, g, "cpu", (3, 4)),
+                              on_final=lambda name: seen.append((name, streams.now)))
+    assert seen == [(n, "side") for n in ("head", "layer0", "embed")]
+    assert set(streams.made[:3]) == {"side"}
+    stack.stack_backward(cfg, table, [{}], g, table, ids, ids, w)
+    assert streams.made[-1] is None and streams.now is None
