@@ -134,3 +134,47 @@ def test_the_stack_allocates_and_clears_on_its_stream(monkeypatch):
     assert set(streams.made[:3]) == {"side"}
     stack.stack_backward(cfg, table, [{}], g, table, ids, ids, w)
     assert streams.made[-1] is None and streams.now is None
+
+
+# ----------------------------------------------------------------------------- gradient lists
+@pytest.fixture
+def clip_calls(monkeypatch):
+    """The calls that reach the library, which is a fake; CPU tensors pass for device tensors."""
+    calls = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: 512 if name.endswith("size") else calls.append(name) or 0
+    monkeypatch.setattr(sbp, "load", Lib)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    monkeypatch.setattr(sbp, "_on_device", lambda stream, *t: (0, None))
+    return calls
+
+
+@pytest.mark.parametrize("n", [1, 12, 16, 17, 40])
+def test_a_list_whose_tensors_got_other_memory_is_refused(clip_calls, n):
+    ws, norm, sq = torch.empty(512, dtype=torch.uint8), torch.zeros(1), torch.zeros(1).double()
+    turns = -(-n // sbp.GradList.LOOK)
+    for k in {0, n // 2, n - 1}:
+        for out in (False, True):
+            old = [torch.full((8,), 3.0) for _ in range(2 * n)]
+            grads, into = sbp.GradList(old[:n]), sbp.GradList(old[n:])
+            for _ in range(2 * turns):
+                sbp.grad_clip_norm(grads, 1.0, norm, out=into if out else None, ws=ws)
+            moved = old[n + k if out else k]
+            kept = (into if out else grads).memory[k]
+            moved.data = torch.zeros(8)
+            del clip_calls[:]
+            with pytest.raises(ValueError, match="other memory"):
+                for _ in range(turns):
+                    sbp.grad_clip_norm(grads, 1.0, norm, out=into if out else None, ws=ws)
+            assert len(clip_calls) == k // sbp.GradList.LOOK
+            # what the calls worked on until then is not freed
+            assert kept.data_ptr() == (into if out else grads).ptrs[k] and kept.nbytes() == 32
+            assert torch.tensor([], dtype=torch.float32).set_(kept).tolist() == [3.0] * 8
+    grads = sbp.GradList([moved])
+    moved.data = torch.zeros(8)
+    for call in (lambda: sbp.grad_sqsum(grads, sq, ws=ws),
+                 lambda: sbp.grad_clip(grads, sq, 1.0, norm_out=norm)):
+        with pytest.raises(ValueError, match="other memory"):
+            call()
