@@ -62,6 +62,7 @@ class ShardedGrads:
         if world < 1 or not 0 <= rank < world:
             raise ValueError(f"bad rank {rank} of world {world}")
         self.world, self.rank = world, rank
+        self.group = None       # the process group that reduces it (GradReducer)
         self.order = [name for name, _ in plan]
         self.flat: Dict[str, object] = {}
         self.out: Dict[str, object] = {}
@@ -106,7 +107,7 @@ class GradReducer:
 
     def __init__(self, grads: ShardedGrads, group=None):
         self.g = grads
-        self.group = group
+        self.group = grads.group = group
         self.works = []
         self.issued: List[str] = []
 
@@ -139,11 +140,20 @@ class GradReducer:
 
 def clip_sharded(grads: ShardedGrads, max_norm: float, group=None, ws=None):
     """Clips this rank's reduced shards in place to the global norm `max_norm` of the whole
-    gradient: the ranks add their sums of squares (one fp64 scalar is exchanged).  Returns the
-    norm before the clipping (device fp32 [1], the same on every rank).  Every rank calls it,
-    after `GradReducer.wait`."""
+    gradient: the ranks of the group that reduced it add their sums of squares (one fp64 scalar is
+    exchanged).  Returns the norm before the clipping (device fp32 [1], the same on every rank).
+    Every rank of the group calls it, after `GradReducer.wait`.  `group` is needed only where no
+    GradReducer was made for `grads`; it cannot be another than the reducer's, in which shards
+    would be counted twice or not at all."""
     import torch
     import torch.distributed as dist
+    if group is None:
+        group = grads.group
+    elif grads.group is not None and group is not grads.group:
+        raise ValueError("clip_sharded: the gradients are reduced by another process group")
+    ranks = dist.get_world_size(group) if group is not None or dist.is_initialized() else 1
+    if ranks != grads.world:
+        raise ValueError(f"clip_sharded: gradients in {grads.world} shards, a group of {ranks}")
     shards = sbp.GradList([grads.out[b] for b in grads.order])
     dev = shards.tensors[0].device
     sqsum = torch.empty(1, dtype=torch.float64, device=dev)

@@ -178,3 +178,73 @@ def test_a_list_whose_tensors_got_other_memory_is_refused(clip_calls, n):
                  lambda: sbp.grad_clip(grads, sq, 1.0, norm_out=norm)):
         with pytest.raises(ValueError, match="other memory"):
             call()
+
+
+# ------------------------------------------------------------------------- sharded gradients
+class _Tensors:
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+
+
+def _subgroup_worker(rank, world, port, q):
+    """Every rank a replica group of its own: the exchange must stay inside it.  The kernels are
+    replaced by their definitions."""
+    import torch.distributed as dist
+
+    from memory_efficient_exact_chunk_b200 import dp
+    dist.init_process_group("gloo", init_method=f"tcp://127.0.0.1:{port}", rank=rank,
+                            world_size=world)
+    sbp.GradList = _Tensors
+    sbp.grad_sqsum = lambda g, out, ws=None: out.copy_(
+        sum(t.double().square().sum() for t in g.tensors).reshape(1))
+    sbp.grad_clip = lambda g, sqsum, max_norm, norm_out=None: norm_out.copy_(sqsum.sqrt())
+    own = [dist.new_group([r]) for r in range(world)][rank]
+    both = dist.new_group(list(range(world)))
+
+    def grads(shards):
+        g = dp.ShardedGrads([("a", [("x", (300,))])], shards, rank % shards, "cpu")
+        g.out["a"].fill_(rank + 1.0)
+        return g
+
+    def refused(*args):
+        try:
+            dp.clip_sharded(*args)
+        except ValueError:
+            return True
+        return False
+    alone, halves, unreduced = grads(1), grads(world), grads(world)
+    dp.GradReducer(alone, group=own)
+    dp.GradReducer(halves, group=both)
+    n = alone.out["a"].numel()
+    got = {"alone": float(dp.clip_sharded(alone, 1.0)) / n ** 0.5,
+           "halves": float(dp.clip_sharded(halves, 1.0)) / halves.out["a"].numel() ** 0.5,
+           "by name": float(dp.clip_sharded(unreduced, 1.0, both)) /
+           unreduced.out["a"].numel() ** 0.5,
+           "refused": [refused(alone, 1.0, both), refused(halves, 1.0, own),
+                       refused(unreduced, 1.0, own), refused(grads(1), 1.0)]}
+    q.put((rank, got))
+    dist.barrier()
+    dist.destroy_process_group()
+
+
+def test_clip_sharded_stays_in_the_reducers_group():
+    import socket
+
+    import torch.multiprocessing as mp
+    with socket.socket() as s:
+        s.bind(("127.0.0.1", 0))
+        port = s.getsockname()[1]
+    ctx = mp.get_context("spawn")
+    q = ctx.Queue()
+    ps = [ctx.Process(target=_subgroup_worker, args=(r, 2, port, q)) for r in range(2)]
+    for p in ps:
+        p.start()
+    got = dict(q.get(timeout=120) for _ in ps)
+    for p in ps:
+        p.join(timeout=60)
+        assert p.exitcode == 0
+    for rank, r in got.items():
+        assert r["refused"] == [True] * 4
+        assert abs(r["alone"] - (rank + 1)) < 1e-5
+        for name in ("halves", "by name"):           # 1 and 2, in halves of equal size
+            assert abs(r[name] - 5 ** 0.5) < 1e-5, name
