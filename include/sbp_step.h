@@ -56,7 +56,7 @@ sbp_status sbp_embedding_scaled_backward(int64_t rows, int64_t cols, int64_t voc
  * 16-byte aligned pointers, ld a multiple of 16 bytes and head_dim a multiple of 16 take the
  * vector path.  Inputs and outputs may be the same buffer (with the same ld); they must not
  * overlap in any other way.  n_kv_heads = 0 leaves the keys out (their pointers are not read).
- * rows < 2^30, rows x heads < 2^31 (else SBP_ERR_UNSUPPORTED).
+ * rows < 2^30, heads <= 65536, rows x heads < 2^31 (else SBP_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------------------------ */
 typedef struct {
   int64_t rows, n_heads, n_kv_heads, head_dim; /* head_dim even, <= 256                        */
@@ -100,7 +100,8 @@ sbp_status sbp_qk_norm_rope_backward(const sbp_qk_cfg* cfg, const void* q, int64
  * Arguments, layouts, accumulation and errors are those of sbp_decoder_layer_forward_stream and
  * sbp_decoder_layer_backward_stream (or, with `reverse`, its _reverse form).  The projections
  * are rounded to cfg->dtype before the norm; only one chunk of them is kept, the backward forms
- * the keys' again.  dq_g, dk_g: device fp32 [head_dim], accumulated.
+ * the keys' again.  dq_g, dk_g: device fp32 [head_dim], accumulated.  For a chunk's rows (batch x
+ * the longest chunk) and heads the limits of sbp_qk_norm_rope_forward hold.
  */
 typedef struct { /* device [head_dim], cfg.dtype, 16-byte aligned */
   const void *q_g, *k_g;

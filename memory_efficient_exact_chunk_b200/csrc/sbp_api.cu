@@ -249,6 +249,17 @@ sbp_status check_layer_cfg(const sbp_layer_cfg* L) {
   return SBP_OK;
 }
 
+// What the norms of queries and keys ask of a layer besides: their kernels count rows, and the heads
+// of all rows of a chunk, in 32 bits.
+sbp_status check_layer_qk(const sbp_layer_cfg& L) {
+  const int64_t R = L.batch * chunk_max(L.seq_len, L.num_chunks);
+  if (R >= kQkMaxRows || L.n_heads > kQkMaxHeads || R * L.n_heads >= 2 * kQkMaxRows)
+    return fail(SBP_ERR_UNSUPPORTED,
+                "query/key norms: a chunk's rows must be below 2^30, heads at most 65536 and rows x "
+                "heads below 2^31");
+  return SBP_OK;
+}
+
 sbp_status check_weights(const sbp_layer_weights* w, bool* has_bias) {
   if (!w) return fail(SBP_ERR_INVALID_ARG, "weights is NULL");
   const void* req[] = {w->ln1_g, w->wq, w->wk, w->wv, w->wo, w->ln2_g, w->w_gate, w->w_up,
@@ -812,6 +823,8 @@ static sbp_status layer_backward_run(const sbp_layer_cfg* cfg, const sbp_layer_w
                                      const sbp_layer_grads* gr, void* workspace,
                                      size_t workspace_bytes, void* stream, bool reverse) {
   if (sbp_status s = check_layer_cfg(cfg)) return s;
+  if (qk)
+    if (sbp_status s = check_layer_qk(*cfg)) return s;
   bool has_bias = false;
   if (sbp_status s = check_weights(w, &has_bias)) return s;
   if (!gr) return fail(SBP_ERR_INVALID_ARG, "grads is NULL");
@@ -1103,6 +1116,8 @@ static sbp_status layer_forward_run(const sbp_layer_cfg* cfg, const sbp_layer_we
                                     const QkGains* qk, const void* x, void* y, void* workspace,
                                     size_t workspace_bytes, void* stream) {
   if (sbp_status s = check_layer_cfg(cfg)) return s;
+  if (qk)
+    if (sbp_status s = check_layer_qk(*cfg)) return s;
   bool has_bias = false;
   if (sbp_status s = check_weights(w, &has_bias)) return s;
   if (!x || !y || !aligned16(x) || !aligned16(y))
@@ -1164,7 +1179,7 @@ static sbp_status check_qk_gains(const sbp_qk_gains* g) {
 }
 
 size_t sbp_decoder_layer_qk_norm_workspace_size(const sbp_layer_cfg* cfg) {
-  if (check_layer_cfg(cfg) != SBP_OK) return 0;
+  if (check_layer_cfg(cfg) != SBP_OK || check_layer_qk(*cfg) != SBP_OK) return 0;
   Carver c(nullptr);
   LayerPlan p;
   layer_carve(c, *cfg, p, true);

@@ -395,7 +395,9 @@ cudaError_t embed_scaled_bwd(int64_t rows, int64_t cols, int64_t vocab, float sc
                              const int* ids, const float* dy, float* d_table, int accumulate,
                              void* ws, cudaStream_t st);
 
-// per-head RMS norm of queries and keys with RoPE (qk_norm.cu)
+// per-head RMS norm of queries and keys with RoPE (qk_norm.cu): rows below kQkMaxRows, at most
+// kQkMaxHeads heads, rows x heads below twice kQkMaxRows
+constexpr int64_t kQkMaxRows = (int64_t)1 << 30, kQkMaxHeads = 65536;
 struct QkNormHeads {       // the queries or the keys; strides in elements between rows
   int64_t n = 0;           // heads per row (0: absent)
   const void* x = nullptr;     // [rows, n, hd], dt

@@ -70,8 +70,8 @@ sbp_status check_qk(const sbp_qk_cfg* c) {
     return fail(SBP_ERR_INVALID_ARG, "rows, n_heads, head_dim and table_len must be positive");
   if (c->head_dim % 2 != 0 || c->head_dim > 256)
     return fail(SBP_ERR_UNSUPPORTED, "head_dim must be even and <= 256");
-  if (c->rows >= kMaxRows || c->rows * imax(c->n_heads, c->n_kv_heads) >= 2 * kMaxRows ||
-      c->n_heads > 65536 || c->n_kv_heads > 65536)
+  const int64_t heads = imax(c->n_heads, c->n_kv_heads);
+  if (c->rows >= kQkMaxRows || heads > kQkMaxHeads || c->rows * heads >= 2 * kQkMaxRows)
     return fail(SBP_ERR_UNSUPPORTED,
                 "rows must be below 2^30, heads at most 65536 and rows x heads below 2^31");
   if (c->dtype != SBP_F32 && c->dtype != SBP_BF16)

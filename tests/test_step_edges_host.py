@@ -248,3 +248,26 @@ def test_clip_sharded_stays_in_the_reducers_group():
         assert abs(r["alone"] - (rank + 1)) < 1e-5
         for name in ("halves", "by name"):           # 1 and 2, in halves of equal size
             assert abs(r[name] - 5 ** 0.5) < 1e-5, name
+
+
+# ------------------------------------------------------------------- the layer with the norms
+@pytest.mark.parametrize("B,T,H,hd,D", [(1, 1 << 25, 64, 2, 1), (1, 1 << 30, 1, 8, 1),
+                                        (1 << 20, 1 << 11, 4, 2, 4), (1, 8, 65537, 8, 1)])
+def test_layers_whose_chunks_pass_the_norms_limits_are_refused(lib, B, T, H, hd, D):
+    """The norms' kernels count rows and heads in 32 bits (no workspace is given, which is checked
+    behind the sizes: no call gets to a launch)."""
+    import ctypes as C
+    cfg = sbp.layer_cfg(B, T, 64, H, H, hd, 64, 1e-6, 1e4, sbp.SBP_F32, D)
+    none = ("bq", "bk", "bv")
+    ptrs = {n: (FAKE if n not in none else None) for n in sbp.WEIGHT_FIELDS}
+    w, g, gains = sbp.LayerWeights(**ptrs), sbp.LayerGrads(**ptrs), sbp.QkGains(FAKE, FAKE)
+    assert lib.sbp_decoder_layer_qk_norm_workspace_size(C.byref(cfg)) == 0
+    assert lib.sbp_decoder_layer_qk_norm_forward_stream(
+        C.byref(cfg), C.byref(w), C.byref(gains), FAKE, FAKE, None, 0, None) == 2
+    assert lib.sbp_decoder_layer_qk_norm_backward_stream(
+        C.byref(cfg), C.byref(w), C.byref(gains), FAKE, FAKE, FAKE, C.byref(g), FAKE, FAKE, 0,
+        None, 0, None) == 2
+    assert "norms" in lib.sbp_last_error().decode()
+    assert lib.sbp_decoder_layer_workspace_size(C.byref(cfg)) > 0      # without norms as before
+    cfg.num_chunks = min(T, 4 * D) if H <= 65536 else D                # shorter chunks are taken
+    assert (lib.sbp_decoder_layer_qk_norm_workspace_size(C.byref(cfg)) > 0) == (H <= 65536)
