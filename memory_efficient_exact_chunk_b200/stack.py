@@ -87,10 +87,11 @@ def stack_forward(cfg: sbp.LayerCfg, embed, layers: List[dict], final_g, ids, ws
 @_on_its_stream
 def stack_backward_from(cfg: sbp.LayerCfg, layers: List[dict], final_g, lm_w, ids, targets,
                         loss_weights, xs, hf, rstd, ws: Workspaces, grads=None, stream=None,
-                        on_final=None, embed_scale=None):
+                        on_final=None, embed_scale=None, embed_shape=None):
     """The streamed backward of the stack from its checkpoints (with the `embed_scale` of its
     forward).  `grads` (optional) holds fp32
-    gradient buffers to accumulate into (the layout StackResult.grads uses); else fresh zeros.
+    gradient buffers to accumulate into (the layout StackResult.grads uses); else fresh zeros,
+    for which `embed_shape` is the shape of the embedding table.
     `on_final` (optional) is called with "head" once the LM-head and final-norm gradients are
     queued, "layer{l}" after layer l's backward and "embed" at the end: the points after which
     the work on the stream leaves that gradient unchanged."""
@@ -99,7 +100,9 @@ def stack_backward_from(cfg: sbp.LayerCfg, layers: List[dict], final_g, lm_w, id
     N, d = hf.shape
     V = lm_w.shape[0]
     if grads is None:
-        grads = zero_grads(layers, lm_w, final_g, dev)
+        if embed_shape is None:
+            raise ValueError("stack_backward_from needs grads, or embed_shape to make them")
+        grads = zero_grads(layers, lm_w, final_g, dev, embed_shape=embed_shape)
     loss = torch.empty(1, dtype=torch.float32, device=dev)
     dhf = torch.empty(N, d, dtype=torch.float32, device=dev)
     cws = ws.get("lmhead", sbp.lmhead_ce_workspace_size(N, d, V, cfg.num_chunks,

@@ -271,3 +271,20 @@ def test_layers_whose_chunks_pass_the_norms_limits_are_refused(lib, B, T, H, hd,
     assert lib.sbp_decoder_layer_workspace_size(C.byref(cfg)) > 0      # without norms as before
     cfg.num_chunks = min(T, 4 * D) if H <= 65536 else D                # shorter chunks are taken
     assert (lib.sbp_decoder_layer_qk_norm_workspace_size(C.byref(cfg)) > 0) == (H <= 65536)
+
+
+def test_the_backward_makes_its_own_gradients(monkeypatch):
+    """Without gradient buffers it makes them all, the embedding's among them, or says at once what
+    it needs."""
+    monkeypatch.setattr(sbp, "load", _Taker)
+    monkeypatch.setattr(sbp, "_stream", lambda s: None)
+    cfg = sbp.layer_cfg(1, 4, 4, 1, 1, 2, 4, 1e-6, 1e4, sbp.SBP_F32, 1)
+    ids, w = torch.ones(4, dtype=torch.int32), torch.ones(4)
+    head, g, x = torch.ones(3, 4), torch.ones(4), torch.ones(4, 4)
+    seen = []
+    args = (cfg, [{"wq": x}], g, head, ids, ids, w, [x, x], x, w, stack.Workspaces("cpu"))
+    r = stack.stack_backward_from(*args, embed_shape=(5, 4))
+    assert r.grads["embed"].shape == (5, 4) and r.grads["lm_head"].shape == (3, 4)
+    with pytest.raises(ValueError, match="embed_shape"):
+        stack.stack_backward_from(*args, on_final=seen.append)
+    assert not seen
