@@ -46,11 +46,16 @@ struct Heads {        // one of the two tensors (queries or keys)
   int64_t lddx;
 };
 
-// kN lanes share a head: a power of two (8 at head_dim 128; the next one where hd / 16 is none),
-// but 5 and 6 for heads of 80 and 96 in the vector layouts.  A warp takes 32 / kN heads, so two
-// of its lanes are left over there, where 8 lanes a head leave three or two of every eight
-// (backward of 16384 x (28 + 4) heads of 80 in bf16: 81 us, 99 with 8; of 96: 94, 104; heads of 48
-// gain nothing from 3 lanes: fp32 forward 45 us, 37 with 4).
+// kN lanes share a head: a power of two (8 at head_dim 128; the next one where hd / 16 is none), but
+// 5 and 6 for heads of 65 to 96 in the vector layouts: a warp takes 6 or 5 heads there, 4 with 8
+// lanes a head.  16384 x (28 + 4) heads, us, with 8 lanes behind the stroke:
+//              72          80           88          96
+//   fwd bf16   -           42.0 / 46.5  -           43.1 / 47.6
+//   fwd fp32   49.9 / 57.8 53.4 / 60.2  59.2 / 63.7 62.3 / 65.7
+//   bwd bf16   83.6 / 93.0 87.6 / 94.7  98.3 / 98.3 103.0 / 100.7
+//   bwd fp32   80.8 / 97.4 85.5 / 101   95.1 / 105  100.5 / 108
+// Heads of 48 gain nothing from 3 lanes (fp32 forward 45 us, 37 with 4).  9 and 10 lanes for heads to
+// 160 would take 3 heads for 2; they need kernels of their own.
 // A lane holds 8 elements of the first half of a head and the 8 that they are rotated with, so
 // the rotation needs no exchange.  Which 8:
 //   kWide    neighbours: one 16-byte access in bf16
@@ -462,7 +467,7 @@ qk_gain_kernel(int hd, int q_blocks, int blocks, const float* partial,
 
 // lanes that share a head
 int lanes_of(int64_t hd, bool vec) {
-  if (vec && (hd == 80 || hd == 96)) return (int)hd / 16;
+  if (vec && hd > 64 && hd <= 96) return (int)nblk(hd, 16);
   int n = 1;
   while (16 * n < hd) n *= 2;
   return n;

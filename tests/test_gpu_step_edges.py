@@ -232,3 +232,19 @@ def test_a_training_step_on_another_stream():
             for a, b in zip(stack.grad_tensors(got.grads), stack.grad_tensors(want.grads)):
                 assert torch.equal(a, b)
         torch.cuda.synchronize()
+
+
+# ------------------------------------------------- head widths between two powers of two lanes
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,H,Hkv,hd,layout,kind", [
+    (1003, 12, 4, 72, "plain", "any"), (515, 7, 3, 72, "fused", "outside"),
+    (31, 6, 2, 72, "odd", None), (1777, 5, 1, 88, "plain", "any"), (2, 1, 11, 88, "fused", "outside"),
+    (64, 32, 8, 88, "plain", 64), (1, 1, 1, 88, "plain", None), (1, 1, 1, 72, "plain", None),
+    (77, 3, 1, 66, "plain", None), (77, 3, 1, 94, "fused", "any"), (130, 4, 2, 104, "plain", 65),
+    (130, 4, 2, 136, "plain", None), (77, 5, 1, 160, "fused", "any")])
+def test_qk_norm_rope_of_widths_between(rows, H, Hkv, hd, layout, kind, dt):
+    """Widths whose heads share a warp in sixes, fives and, off the vector grid or wider, in powers of
+    two, against the definition in 64 bits with the bounds of the other widths."""
+    from tests import test_gpu_step_ops as ops
+    ops.test_qk_norm_rope_forward(rows, H, Hkv, hd, dt, layout, kind)
+    ops.test_qk_norm_rope_backward(rows, H, Hkv, hd, dt, layout, kind)
