@@ -790,8 +790,10 @@ int64_t slabs_of(int64_t cols) { return nblk(cols, 4 * kThreads); }
 
 // Rows of a unit: long units write few partial rows, short ones leave few sums in a row for a
 // group to wait for; a power of two that gives every SM eight groups' worth of full units
-// (11132 rows of 1112: 16, 30.8 us in all, 34 with 8; 12043 of 2568: 32, 45.6, 51.3 with 8; 64K of
-// 4096: 64).
+// (overwritten tables, Zipf ids, in all: 65536 rows of 4096 into 128256: 64, 485 us, 492 with 32,
+// 528 with 8; 48890 of 440 into 32000: 64, 47.9, 51.0 with 8; 600 of 64 into 512: 8, 8.0, 9.7 with
+// 32.  In between half the unit is up to 6 % faster: 11132 of 1112 into 30000: 32, 49.8, 46.7 with
+// 16).
 int unit_rows(int64_t rows, int64_t cols) {
   const int64_t slabs = slabs_of(cols);
   int unit = kMinUnit;
