@@ -14,7 +14,7 @@ an untied LM head (one sequence of T tokens):
   the library's workspaces, as the C ABI sizes them: the decoder layer's (per-chunk buffers,
       O(T / D), plus the K/V prefix and its fp32 gradient, O(T)), the LM head's (O(T / D):
       the logits never leave the chip), and the small ones of the embedding and RMSNorm
-      backward.
+      backward and, where the gradients are clipped, of their norm.
 
 Every workspace figure comes from the library's own *_workspace_size calls, which run on the
 host (no GPU needed), so the model follows the library as it is built.  max_tokens() searches
@@ -41,6 +41,9 @@ class StackShape:
     rms_eps: float = 1e-5
     rope_theta: float = 500000.0
     qkv_bias: bool = False
+    qk_norm: bool = False        # layers with q_norm_g and k_norm_g
+    embed_scaled: bool = False   # embed_scale: the embedding's gradient by sorted tokens
+    clipped: bool = False        # max_grad_norm
 
     @classmethod
     def from_workload(cls, wl):
@@ -54,7 +57,12 @@ class StackShape:
         p = 2 * d + dq * d + 2 * dkv * d + d * dq + 3 * f * d
         if self.qkv_bias:
             p += dq + 2 * dkv
+        if self.qk_norm:
+            p += 2 * self.head_dim
         return p
+
+    def grad_tensors(self) -> int:
+        return 3 + self.n_layers * (9 + 3 * self.qkv_bias + 2 * self.qk_norm)
 
     def params(self) -> int:
         return self.n_layers * self.layer_params() + 2 * self.vocab * self.d_model + self.d_model
@@ -66,10 +74,14 @@ def stack_step_bytes(shape: StackShape, T: int, D: int) -> Dict[str, int]:
     d = shape.d_model
     cfg = sbp.layer_cfg(1, T, d, shape.n_heads, shape.n_kv_heads, shape.head_dim, shape.ffn,
                         shape.rms_eps, shape.rope_theta, sbp.SBP_BF16, D)
-    layer_ws = sbp.layer_workspace_size(cfg)
+    layer_ws = sbp.layer_workspace_size(cfg, shape.qk_norm)
     head_ws = sbp.lmhead_ce_workspace_size(T, d, shape.vocab, D, sbp.SBP_BF16)
     if layer_ws == 0 or head_ws == 0:
         raise ValueError(f"invalid sizes T={T} D={D}")
+    embed_ws = (sbp.embedding_scaled_backward_workspace_size(T, d, shape.vocab)
+                if shape.embed_scaled
+                else int(lib.sbp_embedding_backward_workspace_size(T, shape.vocab)))
+    clip_ws = sbp.grad_norm_workspace_size(shape.grad_tensors()) if shape.clipped else 0
     out = {
         "weights_bf16": 2 * shape.params(),
         "grads_fp32": 4 * shape.params(),
@@ -78,8 +90,7 @@ def stack_step_bytes(shape: StackShape, T: int, D: int) -> Dict[str, int]:
         "residual_grads_fp32": 2 * T * d * 4,                  # dhf, dx
         "layer_workspace": layer_ws,
         "lmhead_workspace": head_ws,
-        "small_workspaces": int(lib.sbp_embedding_backward_workspace_size(T, shape.vocab)) +
-        int(lib.sbp_rmsnorm_backward_workspace_size(T, d)),
+        "small_workspaces": embed_ws + int(lib.sbp_rmsnorm_backward_workspace_size(T, d)) + clip_ws,
     }
     out["total"] = sum(out.values())
     return out

@@ -288,3 +288,28 @@ def test_the_backward_makes_its_own_gradients(monkeypatch):
     with pytest.raises(ValueError, match="embed_shape"):
         stack.stack_backward_from(*args, on_final=seen.append)
     assert not seen
+
+
+# ------------------------------------------------------------------------------ memory model
+def test_memory_model_counts_the_step_operators(lib):
+    """The workspaces that the stack takes for scaled embeddings, normed layers and clipping, and the
+    gains with their gradients."""
+    import dataclasses
+
+    from memory_efficient_exact_chunk_b200 import memory_model as MM
+    from memory_efficient_exact_chunk_b200 import synth
+    plain = MM.StackShape.from_workload(synth.WORKLOADS["llama3_8b_stack4_64k"])
+    T, D, d, V = 65536, 8, plain.d_model, plain.vocab
+    a = MM.stack_step_bytes(plain, T, D)
+    with_all = dataclasses.replace(plain, qk_norm=True, embed_scaled=True, clipped=True)
+    b = MM.stack_step_bytes(with_all, T, D)
+    cfg = sbp.layer_cfg(1, T, d, 32, 8, 128, 14336, 1e-5, 500000.0, sbp.SBP_BF16, D)
+    assert b["layer_workspace"] == sbp.layer_workspace_size(cfg, True) > a["layer_workspace"]
+    assert b["small_workspaces"] - a["small_workspaces"] == (
+        sbp.embedding_scaled_backward_workspace_size(T, d, V)
+        - int(lib.sbp_embedding_backward_workspace_size(T, V))
+        + sbp.grad_norm_workspace_size(3 + 4 * 11))
+    assert b["small_workspaces"] - a["small_workspaces"] > 30e6        # the partial rows
+    assert b["grads_fp32"] - a["grads_fp32"] == 4 * 4 * 2 * 128
+    assert b["total"] == sum(v for k, v in b.items() if k != "total")
+    assert MM.max_tokens(with_all, D, 150 * 10 ** 9) < MM.max_tokens(plain, D, 150 * 10 ** 9)
