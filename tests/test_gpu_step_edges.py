@@ -248,3 +248,27 @@ def test_qk_norm_rope_of_widths_between(rows, H, Hkv, hd, layout, kind, dt):
     from tests import test_gpu_step_ops as ops
     ops.test_qk_norm_rope_forward(rows, H, Hkv, hd, dt, layout, kind)
     ops.test_qk_norm_rope_backward(rows, H, Hkv, hd, dt, layout, kind)
+
+
+# --------------------------------------------------------- gains of a bf16 layer, few summands
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("H,Hkv,B,T,D", [(1, 1, 1, 2, 2), (1, 1, 1, 2, 1), (2, 1, 1, 2, 2),
+                                         (1, 1, 1, 3, 3), (1, 1, 2, 2, 2), (2, 2, 1, 3, 2)])
+def test_bf16_gain_gradients_of_few_summands(H, Hkv, B, T, D, reverse):
+    """The upstream gradient reaches the last token alone, so a gain's gradient is a sum of few
+    products that hardly cancel (which is asserted), and rows of another chunk or of another
+    rounding would show.  A summand passes ten roundings to bf16 on its way (n1, the projection,
+    q, k, v, dy, dh, dO, O, and P or dS), of 2^-8 at most each: 5e-2 of the summands' magnitudes,
+    a tenth of the result."""
+    from tests import test_gpu_step_layer as layer
+    L = S(256, H, Hkv, 128, 512, 1e-6, 10000.0)
+    W = layer.make_layer(L, 10 * T + D + H, "bf16")
+    g = gen(100 * B + 10 * T + H)
+    x = torch.randn(B, T, L.d_model, generator=g, device="cuda").bfloat16()
+    dy = torch.zeros(B, T, L.d_model, device="cuda")
+    dy[:, -1] = torch.randn(B, L.d_model, generator=g, device="cuda") * 1e-3
+    _, _, want, mags = layer.ref_backward(L, W, x, dy)
+    _, _, got = layer.gpu_backward(L, W, x, dy, D, reverse)
+    for n in sbp.QK_NORM_FIELDS:
+        assert mags[n] <= 2 * float(want[n].norm()), n
+        assert float((got[n].double() - want[n]).norm()) <= 5e-2 * mags[n], n
