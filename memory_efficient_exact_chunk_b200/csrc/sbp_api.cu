@@ -4,13 +4,12 @@
 // Sources: "StreamBP: Memory-Efficient Backpropagation" (skill page), sections Core Concept,
 // Architecture Overview and Implementation; "StreamBP: Memory-Efficient Exact Backpropagation
 // for Long Sequence Training of LLMs" (paper page), Abstract.
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
 #include <initializer_list>
 #include <mutex>
 #include <string>
 
+#include "api_checks.cuh"
 #include "sbp.h"
 #include "sbp_debug.h"
 #include "sbp_dpo.h"
@@ -25,25 +24,6 @@ thread_local std::string g_err;
 // status word of the workspace of the entry point running on this thread (GEMMs raise their
 // bounded-wait timeouts there)
 thread_local int* tl_status = nullptr;
-
-sbp_status fail(sbp_status s, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_err = buf;
-  return s;
-}
-
-#define SBP_CK(expr)                                                                 \
-  do {                                                                               \
-    cudaError_t e_ = (expr);                                                         \
-    if (e_ != cudaSuccess)                                                           \
-      return fail(SBP_ERR_CUDA, "%s failed: %s", #expr, cudaGetErrorString(e_));     \
-  } while (0)
-
-inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 // Bump allocator over the caller's workspace (dry run when base == nullptr).
 struct Carver {
@@ -456,14 +436,6 @@ sbp_status layer_chunk_forward(const sbp_layer_cfg& L, const sbp_layer_weights& 
     SBP_CK(gemm(gup, st));
     SBP_CK(swiglu_fwd(R, f, dt, p.gu, p.m, st));
   }
-  return SBP_OK;
-}
-
-sbp_status check_ws(void* ws, size_t have, size_t need) {
-  if (!ws) return fail(SBP_ERR_INVALID_ARG, "workspace is NULL");
-  if (((uintptr_t)ws & 255u) != 0) return fail(SBP_ERR_INVALID_ARG, "workspace not 256-byte aligned");
-  if (have < need)
-    return fail(SBP_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", have, need);
   return SBP_OK;
 }
 

@@ -1,47 +1,16 @@
 // C ABI of the operators around the streamed step (include/sbp_step.h): argument checks and
 // workspace layout; the kernels are in embedding.cu, qk_norm.cu and grad_norm.cu.
-#include <cmath>
-#include <cstdarg>
-#include <cstdio>
-
-#include "sbp_internal.cuh"
+#include "api_checks.cuh"
 #include "sbp_step.h"
 
 using namespace sbp;
 
 namespace {
 
-sbp_status fail(sbp_status s, const char* fmt, ...) {
-  char buf[256];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  set_last_error(buf);
-  return s;
-}
-
-#define STEP_CK(expr)                                                              \
-  do {                                                                             \
-    const cudaError_t e_ = (expr);                                                 \
-    if (e_ != cudaSuccess)                                                         \
-      return fail(SBP_ERR_CUDA, "%s failed: %s", #expr, cudaGetErrorString(e_));   \
-  } while (0)
-
-inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
 // whether two ranges of n bytes have bytes in common
 inline bool overlap(const void* p, const void* q, size_t n) {
   const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
   return a < b + n && b < a + n;
-}
-
-sbp_status check_ws(void* ws, size_t have, size_t need) {
-  if (!ws) return fail(SBP_ERR_INVALID_ARG, "workspace is NULL");
-  if (!aligned(ws, 256)) return fail(SBP_ERR_INVALID_ARG, "workspace not 256-byte aligned");
-  if (have < need)
-    return fail(SBP_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", have, need);
-  return SBP_OK;
 }
 
 // ------------------------------------------------------------------------ embedding
@@ -167,7 +136,7 @@ sbp_status sbp_embedding_scaled_forward(int64_t rows, int64_t cols, int64_t voca
                                         float scale, const int32_t* ids, const void* table,
                                         void* y, void* stream) {
   if (sbp_status s = check_embed(rows, cols, vocab, dt, ids, table, y)) return s;
-  STEP_CK(embed_scaled_fwd(rows, cols, vocab, dt, scale, ids, table, y,
+  SBP_CK(embed_scaled_fwd(rows, cols, vocab, dt, scale, ids, table, y,
                            static_cast<cudaStream_t>(stream)));
   return SBP_OK;
 }
@@ -187,7 +156,7 @@ sbp_status sbp_embedding_scaled_backward(int64_t rows, int64_t cols, int64_t voc
   if (sbp_status s = check_ws(workspace, workspace_bytes,
                               embed_scaled_bwd_ws_bytes(rows, cols, vocab)))
     return s;
-  STEP_CK(embed_scaled_bwd(rows, cols, vocab, scale, ids, dy, d_table, accumulate, workspace,
+  SBP_CK(embed_scaled_bwd(rows, cols, vocab, scale, ids, dy, d_table, accumulate, workspace,
                            static_cast<cudaStream_t>(stream)));
   return SBP_OK;
 }
@@ -201,7 +170,7 @@ sbp_status sbp_rope_table(int64_t positions, int64_t head_dim, double theta, flo
   if (!(theta > 0.0)) return fail(SBP_ERR_INVALID_ARG, "theta must be > 0");
   if (!cos_table || !sin_table || !aligned(cos_table, 16) || !aligned(sin_table, 16))
     return fail(SBP_ERR_INVALID_ARG, "a table pointer is NULL or not 16-byte aligned");
-  STEP_CK(rope_table(positions, head_dim, theta, cos_table, sin_table,
+  SBP_CK(rope_table(positions, head_dim, theta, cos_table, sin_table,
                      static_cast<cudaStream_t>(stream)));
   return SBP_OK;
 }
@@ -221,7 +190,7 @@ sbp_status sbp_qk_norm_rope_forward(const sbp_qk_cfg* cfg, const void* q, int64_
   a.q.ldy = ldqo;
   a.k.y = k_out;
   a.k.ldy = ldko;
-  STEP_CK(qk_norm_rope_fwd(a, static_cast<cudaStream_t>(stream)));
+  SBP_CK(qk_norm_rope_fwd(a, static_cast<cudaStream_t>(stream)));
   return SBP_OK;
 }
 
@@ -259,7 +228,7 @@ sbp_status sbp_qk_norm_rope_backward(const sbp_qk_cfg* cfg, const void* q, int64
   a.k.lddy = lddko;
   a.k.dx = dk;
   a.k.lddx = lddk;
-  STEP_CK(qk_norm_rope_bwd(a, dq_g, dk_g, static_cast<float*>(workspace),
+  SBP_CK(qk_norm_rope_bwd(a, dq_g, dk_g, static_cast<float*>(workspace),
                            static_cast<cudaStream_t>(stream)));
   return SBP_OK;
 }
@@ -273,7 +242,7 @@ sbp_status sbp_grad_sqsum(int64_t n, const float* const* grads, const int64_t* n
   if (sbp_status s = check_grads(n, grads, nullptr, numel)) return s;
   if (!sqsum || !aligned(sqsum, 8)) return fail(SBP_ERR_INVALID_ARG, "sqsum NULL or misaligned");
   if (sbp_status s = check_ws(workspace, workspace_bytes, grad_norm_ws_bytes(n))) return s;
-  STEP_CK(grad_sqsum(tensors_of(n, grads, nullptr, numel), sqsum, workspace,
+  SBP_CK(grad_sqsum(tensors_of(n, grads, nullptr, numel), sqsum, workspace,
                      static_cast<cudaStream_t>(stream)));
   return SBP_OK;
 }
@@ -285,7 +254,7 @@ sbp_status sbp_grad_clip(int64_t n, const float* const* grads, float* const* out
   if (!sqsum || !aligned(sqsum, 8)) return fail(SBP_ERR_INVALID_ARG, "sqsum NULL or misaligned");
   if (sbp_status s = check_max_norm(max_norm)) return s;
   if (!aligned(norm_out, 4)) return fail(SBP_ERR_INVALID_ARG, "norm_out is misaligned");
-  STEP_CK(grad_clip(tensors_of(n, grads, outs, numel), sqsum, max_norm, norm_out,
+  SBP_CK(grad_clip(tensors_of(n, grads, outs, numel), sqsum, max_norm, norm_out,
                     static_cast<cudaStream_t>(stream)));
   return SBP_OK;
 }
@@ -298,7 +267,7 @@ sbp_status sbp_grad_clip_norm(int64_t n, const float* const* grads, float* const
   if (!norm_out || !aligned(norm_out, 4))
     return fail(SBP_ERR_INVALID_ARG, "norm_out is NULL or misaligned");
   if (sbp_status s = check_ws(workspace, workspace_bytes, grad_norm_ws_bytes(n))) return s;
-  STEP_CK(grad_clip_norm(tensors_of(n, grads, outs, numel), max_norm, norm_out, workspace,
+  SBP_CK(grad_clip_norm(tensors_of(n, grads, outs, numel), max_norm, norm_out, workspace,
                          static_cast<cudaStream_t>(stream)));
   return SBP_OK;
 }
