@@ -222,7 +222,10 @@ def workspace(nbytes: int, device="cuda", stream=None):
     calls on `stream`."""
     torch = _torch()
     with allocating(stream):
-        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+        t = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    if stream is not None and t.is_cuda:      # it may be passed to calls on the current one too
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
 
 
 def device_status(ws, stream=None):

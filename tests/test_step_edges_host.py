@@ -313,3 +313,20 @@ def test_memory_model_counts_the_step_operators(lib):
     assert b["grads_fp32"] - a["grads_fp32"] == 4 * 4 * 2 * 128
     assert b["total"] == sum(v for k, v in b.items() if k != "total")
     assert MM.max_tokens(with_all, D, 150 * 10 ** 9) < MM.max_tokens(plain, D, 150 * 10 ** 9)
+
+
+def test_a_workspace_for_another_stream_may_come_back_to_the_current_one(monkeypatch):
+    """It is returned to the caller, who may use it on either: its memory is not handed out again
+    before both have passed its end."""
+    class Buffer:
+        is_cuda, device, recorded = True, "cuda:0", []
+
+        def record_stream(self, stream):
+            self.recorded.append(stream)
+    streams = _Streams(monkeypatch)
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: Buffer())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: (d, streams.now))
+    sbp.workspace(100, "cuda:0", "side")
+    assert Buffer.recorded == [("cuda:0", None)]
+    sbp.workspace(100, "cuda:0")
+    assert len(Buffer.recorded) == 1
